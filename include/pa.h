@@ -65,7 +65,8 @@ typedef enum pa_dtype {
   PA_I32 = 1,
   PA_I64 = 2,
   PA_F8E4M3 = 3, /* one byte: 1 sign, 4 exponent (bias 7), 3 mantissa bits; 0x7F/0xFF NaN, max 448 */
-  PA_BF16 = 4    /* bfloat16: 1 sign, 8 exponent (bias 127), 7 mantissa bits */
+  PA_BF16 = 4,   /* bfloat16: 1 sign, 8 exponent (bias 127), 7 mantissa bits */
+  PA_F32 = 5     /* IEEE binary32: weights of pa_diff_attention only */
 } pa_dtype;
 
 typedef struct pa_tensor {
@@ -267,6 +268,115 @@ int pa_set_stream_error_word(void* stream, uint32_t* device_word);
  * pa_get_device_error.  n = 0 is a no-op.
  */
 int pa_copy_blocks(const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* pairs,
+                   void* stream);
+
+/*
+ * pa_rope_and_cache -- rotary positions with one or several axes, and the step's K/V into their
+ * slots: q is rotated into q_out, k rotated and v unchanged are written as pa_reshape_and_cache
+ * writes them.  (No paper counterpart: the pages take rotated keys as given.)
+ *
+ * Of every q and k head, pair i < num_pairs turns by theta = positions[axis_of_pair[i]][t] *
+ * inv_freq[i]: (a, b) -> factor * (a cos theta - b sin theta, b cos theta + a sin theta), where
+ * (a, b) are dims (i, i + num_pairs), or (2i, 2i + 1) when `adjacent`.  Dims from 2 * num_pairs
+ * on are copied.  Several axes are the time, height and width of an image or video token; text
+ * gives every axis the same position.
+ *   q               fp16 or bf16 [T, Hq, d]; token stride free (multiple of 8), head stride d.
+ *   k, v            same type [T, Hkv, d], strides as q's.
+ *   positions       int64 [A, T], A in 1..255; axis stride free.  Any value, also negative;
+ *                   angles are exact to float32 for |position| < 2^31.
+ *   rope            HOST struct and HOST arrays, read before the call returns.
+ *   k_cache,v_cache [NB, Hkv, bs, d] of q's type, or PA_F8E4M3 (fp16 q, k, v) with scales: a
+ *                   value's code is E4M3(x * (1 / scale)) of the unrounded rotated x.
+ *   slot_mapping    int64 [T] as in pa_reshape_and_cache: negative slots write no K/V (q is
+ *                   rotated all the same), slots past the pool are reported.
+ *   q_out           [T, Hq, d] of q's type, strides as q's; q itself (in place) or memory that
+ *                   overlaps neither q, k nor v.
+ *   scales          required for PA_F8E4M3 pools, else ignored (may be NULL).
+ * Arithmetic is float32 with one rounding per output.  Supported: d in {64, 128}, bs in
+ * {16, 32}, num_pairs a multiple of 8 up to d / 2.
+ */
+typedef struct pa_rope {
+  int32_t num_pairs;           /* R / 2 rotated pairs per head */
+  int32_t adjacent;            /* 0: pair (i, i + num_pairs); 1: pair (2i, 2i + 1) */
+  float factor;                /* multiplies cos and sin (1 normally) */
+  const double* inv_freq;      /* [num_pairs] radians per position */
+  const int32_t* axis_of_pair; /* [num_pairs] axis of each pair; NULL: axis 0 for all */
+} pa_rope;
+
+int pa_rope_and_cache(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v,
+                      const pa_tensor* positions, const pa_rope* rope, const pa_tensor* k_cache,
+                      const pa_tensor* v_cache, const pa_tensor* slot_mapping,
+                      const pa_tensor* q_out, const pa_kv_scales* scales, void* stream);
+
+/*
+ * pa_diff_attention -- differential attention for one mixed continuous-batching step: the
+ * difference of two softmax maps with learned weights, over the same pools, tables and batch
+ * description as pa_attention.  (No paper counterpart.)
+ *
+ * Heads come in pairs: q heads 2p and 2p + 1 are the queries of the two maps of differential head
+ * p; K heads 2j and 2j + 1 hold the two maps' keys and V heads 2j, 2j + 1 the halves of one
+ * 2d-wide value, j = p / (Hq / Hkv).  For each row, over the keys it sees in pa_attention:
+ *   y = softmax(scale q_2p K_2j^T) [V_2j | V_2j+1] - lambda_p softmax(scale q_2p+1 K_2j+1^T) [...]
+ *   out = out_scale * y * rsqrt(mean(y^2) + eps) * norm_weight     (without norm_weight:
+ *   out = out_scale * y)
+ *   q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, hint, workspace
+ *                    as in pa_attention, with Hkv (and so Hq) even, fp16 or bf16;
+ *                    hint->shared_prefix_tokens must be 0.
+ *   diff->lambda     float32 [Hq / 2], or [T, Hq / 2] (token stride free): one per token and head.
+ *   diff->norm_weight float32 [2d] or NULL.
+ *   out              [T, Hq / 2, 2d] of q's type, contiguous.
+ *   workspace        device scratch of pa_diff_attention_workspace_size(...) bytes for the same
+ *                    number of sequences, heads and hint; 256-byte aligned.
+ * Rows of sequences that the device finds invalid are left unwritten and reported, as in
+ * pa_attention.  The weights of a row's hidden keys are 0, but a V value of NaN or infinity at a
+ * key that some row of the same chunk sees may reach the chunk's other rows (0 * infinity).
+ * Supported: d in {64, 128}, bs in {16, 32}, Hq / Hkv in 1..16; not over FP8 pools.
+ */
+typedef struct pa_diff {
+  const pa_tensor* lambda;
+  const pa_tensor* norm_weight; /* NULL: no norm */
+  float eps;                    /* >= 0 */
+  float out_scale;
+} pa_diff;
+
+size_t pa_diff_attention_workspace_size(int64_t num_seqs, int64_t num_q_heads,
+                                        int64_t num_kv_heads, int64_t head_dim,
+                                        const pa_batch_hint* hint);
+
+int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                      const pa_tensor* block_tables, const pa_tensor* seq_lens,
+                      const pa_tensor* query_start_loc, float scale, const pa_diff* diff,
+                      const pa_tensor* out, const pa_batch_hint* hint, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * pa_move_blocks -- move whole physical blocks inside the pool, in place, and give block tables
+ * their new ids: the device side of a compaction (pa_bm_compact), in which a block may move into
+ * one that moves on itself (chains and cycles, which pa_copy_blocks does not take).
+ *
+ * pa_move_plan_create takes n HOST pairs (src, dst): no two moves out of one block, no two into
+ * one block, ids inside the pool; src = dst is no move.  NULL on error (pa_last_error).  The plan
+ * holds no device memory and serves any number of pools of num_blocks blocks.
+ *   k_cache, v_cache  [NB, Hkv, bs, d], or all layers at once: [L, NB, Hkv, bs, d] (each layer
+ *                     contiguous, layer stride free), fp16, bf16 or PA_F8E4M3.
+ *   block_tables      int32 [N, MB] (row stride free) or NULL: every entry that is a moved
+ *                     block's old id becomes its new id; other entries, ids outside the pool
+ *                     among them, stay.  Pass it with one call where pools are moved by several.
+ *   workspace         pa_move_blocks_workspace_size(plan, k_cache, 1, block_tables != NULL) bytes
+ *                     at least, 256-byte aligned (NULL allowed when that is 0); with room for
+ *                     more layers, more are moved per launch.
+ * After the call, block dst holds what block src held before it, for every pair; a block that
+ * only moved out keeps its old content.  pa_move_plan_staged: blocks that pass through the
+ * workspace (0 unless long chains or cycles meet).
+ */
+typedef struct pa_move_plan pa_move_plan;
+pa_move_plan* pa_move_plan_create(const int32_t* pairs, int64_t n, int64_t num_blocks);
+void pa_move_plan_destroy(pa_move_plan* plan);
+int64_t pa_move_plan_staged(const pa_move_plan* plan);
+size_t pa_move_blocks_workspace_size(const pa_move_plan* plan, const pa_tensor* k_cache,
+                                     int32_t layers, int32_t with_tables);
+int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                   const pa_tensor* block_tables, void* workspace, size_t workspace_bytes,
                    void* stream);
 
 /*

@@ -78,6 +78,18 @@ int pa_bm_fork(pa_block_manager* bm, int64_t parent, int64_t child);
 /* Release seq_id and all its block references. */
 int pa_bm_free(pa_block_manager* bm, int64_t seq_id);
 
+/* Renumber the blocks in use (referenced or cached) to 0 .. used - 1, so that the free ones are
+ * the pool's tail.  in_order = 0 moves as few blocks as possible: those past `used` into the
+ * holes before it.  in_order = 1 lays sequences out one after the other, by ascending id, each in
+ * logical order (a shared block at its first use), then the cached unused blocks, least recently
+ * released first: a sequence's private blocks are then one contiguous range.
+ * moves receives (old, new) id pairs, *num_moves of them (room for max_moves pairs; at most
+ * num_blocks): the caller runs them through pa_move_blocks before the pool's next use.  Block
+ * tables made before the call hold old ids.  PA_ERR_INVALID_ARG when moves is too small or out of
+ * host memory (nothing changed). */
+int pa_bm_compact(pa_block_manager* bm, int32_t in_order, int32_t* moves, int32_t max_moves,
+                  int32_t* num_moves);
+
 /* Counts: free blocks (not cached, unused), evictable blocks (cached, unused), cached blocks
  * (in the prefix cache, used or not), live sequences.  Any pointer may be NULL. */
 int pa_bm_stats(const pa_block_manager* bm, int32_t* free_blocks, int32_t* evictable_blocks,

@@ -29,7 +29,7 @@ PA_ERR_NO_BLOCKS = 8
 STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_CUDA",
                 4: "PA_ERR_TIMEOUT", 5: "PA_ERR_OUT_OF_RANGE", 6: "PA_ERR_WORKSPACE",
                 7: "PA_ERR_DESCRIPTOR", 8: "PA_ERR_NO_BLOCKS"}
-PA_F16, PA_I32, PA_I64, PA_F8E4M3, PA_BF16 = 0, 1, 2, 3, 4
+PA_F16, PA_I32, PA_I64, PA_F8E4M3, PA_BF16, PA_F32 = 0, 1, 2, 3, 4, 5
 PA_WAIT_LIMIT_DEFAULT_NS = 2_000_000_000
 PARTITION_TOKENS = 512
 EXPORTED = ("pa_reshape_and_cache", "pa_attention_workspace_size", "pa_attention",
@@ -39,11 +39,15 @@ EXPORTED = ("pa_reshape_and_cache", "pa_attention_workspace_size", "pa_attention
             "pa_bm_create", "pa_bm_destroy", "pa_bm_add_sequence", "pa_bm_append",
             "pa_bm_truncate", "pa_bm_fork", "pa_bm_free", "pa_bm_stats", "pa_bm_sequence",
             "pa_bm_step_descriptor", "pa_step_slot_mapping", "pa_set_wait_limit",
-            "pa_selftest_wait_timeout", "pa_set_stream_error_word")
+            "pa_selftest_wait_timeout", "pa_set_stream_error_word", "pa_rope_and_cache",
+            "pa_diff_attention_workspace_size", "pa_diff_attention", "pa_move_plan_create",
+            "pa_move_plan_destroy", "pa_move_plan_staged", "pa_move_blocks_workspace_size",
+            "pa_move_blocks", "pa_bm_compact")
 
 # Byte tensors are E4M3 codes (the only one-byte type of the ABI).
 _DTYPES = {torch.float16: PA_F16, torch.int32: PA_I32, torch.int64: PA_I64,
-           torch.uint8: PA_F8E4M3, torch.float8_e4m3fn: PA_F8E4M3, torch.bfloat16: PA_BF16}
+           torch.uint8: PA_F8E4M3, torch.float8_e4m3fn: PA_F8E4M3, torch.bfloat16: PA_BF16,
+           torch.float32: PA_F32}
 
 
 class PATensor(ctypes.Structure):
@@ -58,6 +62,17 @@ class PABatchHint(ctypes.Structure):
 
 class PAKVScales(ctypes.Structure):
     _fields_ = [("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class PARope(ctypes.Structure):
+    _fields_ = [("num_pairs", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("inv_freq", ctypes.c_void_p),
+                ("axis_of_pair", ctypes.c_void_p)]
+
+
+class PADiff(ctypes.Structure):
+    _fields_ = [("lam", ctypes.POINTER(PATensor)), ("norm_weight", ctypes.POINTER(PATensor)),
+                ("eps", ctypes.c_float), ("out_scale", ctypes.c_float)]
 
 
 class PAError(RuntimeError):
@@ -126,7 +141,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                 ("pa_bm_step_descriptor", ctypes.c_int,
                  [VP, PI64, PI32, I32, I32, I32, PI32, PI32, PI32, PI64]),
                 ("pa_step_slot_mapping", ctypes.c_int,
-                 [I32, PI32, PI32, PI32, I64, I32, I32, PI32, PI64, I64])):
+                 [I32, PI32, PI32, PI32, I64, I32, I32, PI32, PI64, I64]),
+                ("pa_bm_compact", ctypes.c_int, [VP, I32, PI32, I32, PI32]),
+                ("pa_rope_and_cache", ctypes.c_int,
+                 [P, P, P, P, ctypes.POINTER(PARope), P, P, P, P, S, VP]),
+                ("pa_diff_attention_workspace_size", ctypes.c_size_t,
+                 [I64, I64, I64, I64, ctypes.POINTER(PABatchHint)]),
+                ("pa_diff_attention", ctypes.c_int,
+                 [P, P, P, P, P, P, ctypes.c_float, ctypes.POINTER(PADiff), P,
+                  ctypes.POINTER(PABatchHint), VP, ctypes.c_size_t, VP]),
+                ("pa_move_plan_create", VP, [VP, I64, I64]),
+                ("pa_move_plan_destroy", None, [VP]),
+                ("pa_move_plan_staged", I64, [VP]),
+                ("pa_move_blocks_workspace_size", ctypes.c_size_t, [VP, P, I32, I32]),
+                ("pa_move_blocks", ctypes.c_int, [VP, P, P, P, VP, ctypes.c_size_t, VP])):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -223,6 +251,168 @@ def attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scal
                                 ctypes.byref(describe(out)), ctypes.byref(hint), wptr, wbytes,
                                 _stream_handle(stream)))
     return out
+
+
+def _check_device(*tensors) -> None:
+    """The library runs on the current device and takes device pointers only."""
+    here = torch.cuda.current_device() if all(t.is_cuda for t in tensors) else -1
+    for t in tensors:
+        if not t.is_cuda or t.get_device() != here:
+            raise ValueError(f"every tensor must be on the current CUDA device, got {t.device}")
+
+
+def _workspace(need: int, workspace: Optional[torch.Tensor], device, stream):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one allocated here."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:  # allocated on the current stream, used on another
+            workspace.record_stream(stream)
+    else:
+        _check_device(workspace)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def rope_inv_freq(rotary_dim: int, base: float = 10000.0) -> torch.Tensor:
+    """base^(-2i / rotary_dim) for i < rotary_dim / 2: host float64, as ``rope_and_cache`` takes."""
+    return float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+
+
+def rope_axes(sections) -> torch.Tensor:
+    """The axis of each pair when axis a takes the next ``sections[a]`` pairs (host int32)."""
+    n = torch.as_tensor(list(sections), dtype=torch.int64)
+    return torch.repeat_interleave(torch.arange(len(n), dtype=torch.int32), n)
+
+
+def rope_and_cache(q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, q_out=None,
+                   axes=None, adjacent: bool = False, factor: float = 1.0, stream=None,
+                   k_scale=None, v_scale=None) -> torch.Tensor:
+    """``pa_rope_and_cache``: rotate q [T, Hq, d] into ``q_out`` (returned; a new tensor when
+    omitted, q itself for in place), rotate k and write it and v [T, Hkv, d] into pool slots.
+
+    ``positions`` is int64 [T] or [A, T]; ``inv_freq`` (host float64) holds radians per position
+    of each rotated pair, ``axes`` (host int32) the axis each pair turns with (None: axis 0).
+    Pair i is dims (i, i + len(inv_freq)), or (2i, 2i + 1) when ``adjacent``; cos and sin are
+    multiplied by ``factor``.  A byte pool is an FP8 (E4M3) cache and needs the two scales."""
+    lib = load_library()
+    for name, t, dtype in (("inv_freq", inv_freq, torch.float64), ("axes", axes, torch.int32)):
+        if t is not None and (t.dtype != dtype or t.is_cuda or t.dim() != 1 or
+                              not t.is_contiguous() or t.numel() != inv_freq.numel()):
+            raise ValueError(f"{name} must be a contiguous host {dtype} vector, one entry per pair")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if stream is not None:
+            q_out.record_stream(stream)
+    _check_device(q, k, v, positions, k_cache, v_cache, slot_mapping, q_out)
+    if positions.dim() == 1:
+        positions = positions[None]
+    rope = PARope(inv_freq.numel(), int(bool(adjacent)), float(factor), inv_freq.data_ptr(),
+                  axes.data_ptr() if axes is not None else None)
+    sc = None
+    if _is_fp8(k_cache):
+        sc = ctypes.byref(PAKVScales(float(k_scale), float(v_scale)))
+    d = [ctypes.byref(describe(x)) for x in (q, k, v, positions, k_cache, v_cache, slot_mapping,
+                                             q_out)]
+    _check(lib.pa_rope_and_cache(*d[:4], ctypes.byref(rope), *d[4:], sc, _stream_handle(stream)))
+    return q_out
+
+
+def diff_attention_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                  head_dim: int, max_query_len: int, max_seq_len: int,
+                                  num_prefill_seqs: int = 0) -> int:
+    hint = PABatchHint(int(max_query_len), int(max_seq_len), int(num_prefill_seqs), 0)
+    return int(load_library().pa_diff_attention_workspace_size(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, ctypes.byref(hint)))
+
+
+def diff_attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale: float,
+                   lam, out, max_query_len: int, max_seq_len: int, norm_weight=None,
+                   eps: float = 1e-5, out_scale: float = 1.0,
+                   workspace: Optional[torch.Tensor] = None, stream=None,
+                   num_prefill_seqs: int = 0) -> torch.Tensor:
+    """``pa_diff_attention``: differential attention for one mixed batch; writes ``out``
+    [T, Hq / 2, 2 d] and returns it.
+
+    q heads 2p, 2p + 1 are the two maps' queries of differential head p, K heads 2j, 2j + 1 the
+    two maps' keys, V heads 2j, 2j + 1 the halves of the 2d-wide value.  ``lam`` is float32
+    [Hq / 2] or [T, Hq / 2].  With ``norm_weight`` (float32 [2d]) each head's result is divided by
+    its root mean square (``eps`` inside) and multiplied by it; ``out_scale`` multiplies last.
+    The other arguments are those of ``attention``."""
+    lib = load_library()
+    hint = PABatchHint(int(max_query_len), int(max_seq_len), int(num_prefill_seqs), 0)
+    tensors = [q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, out, lam]
+    if norm_weight is not None:
+        tensors.append(norm_weight)
+    _check_device(*tensors)
+    need = 0
+    if workspace is None and q.dim() == 3 and k_cache.dim() == 4:
+        need = int(lib.pa_diff_attention_workspace_size(
+            seq_lens.numel(), q.shape[1], k_cache.shape[1], q.shape[2], ctypes.byref(hint)))
+    workspace, wptr, wbytes = _workspace(need, workspace, q.device, stream)
+    d = [describe(x) for x in tensors]
+    diff = PADiff(ctypes.pointer(d[7]), ctypes.pointer(d[8]) if norm_weight is not None else None,
+                  float(eps), float(out_scale))
+    r = [ctypes.byref(x) for x in d[:7]]
+    _check(lib.pa_diff_attention(*r[:6], ctypes.c_float(scale), ctypes.byref(diff), r[6],
+                                 ctypes.byref(hint), wptr, wbytes, _stream_handle(stream)))
+    return out
+
+
+class MovePlan:
+    """``pa_move_plan``: an ordered list of block moves (src, dst) for pools of ``num_blocks``
+    blocks, e.g. from ``BlockManager.compact``.  Holds host memory only; any number of
+    ``move_blocks`` calls may use it."""
+
+    def __init__(self, pairs, num_blocks: int):
+        p = torch.as_tensor(pairs, dtype=torch.int32)
+        p = p.reshape(p.numel() // 2, 2).contiguous()
+        if p.is_cuda:
+            raise ValueError("pairs must be on the host")
+        self._lib = load_library()
+        self.num_blocks = int(num_blocks)
+        self._h = self._lib.pa_move_plan_create(p.data_ptr() if p.numel() else None, p.shape[0],
+                                                self.num_blocks)
+        if not self._h:
+            raise PAError(PA_ERR_INVALID_ARG, last_error())
+
+    @property
+    def staged(self) -> int:
+        """Blocks that pass through the workspace."""
+        return int(self._lib.pa_move_plan_staged(self._h))
+
+    def workspace_size(self, k_cache, layers: int = 1, with_tables: bool = True) -> int:
+        return int(self._lib.pa_move_blocks_workspace_size(
+            self._h, ctypes.byref(describe(k_cache)), int(layers), int(bool(with_tables))))
+
+    def close(self):
+        if getattr(self, "_h", None):
+            self._lib.pa_move_plan_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def move_blocks(k_cache, v_cache, plan, block_tables=None,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``pa_move_blocks``: move whole blocks inside the pool, in place, and renumber
+    ``block_tables``.  ``plan`` is a ``MovePlan`` or its pairs (host int32 [n, 2]: src, dst, where
+    a destination may be another pair's source); the pools are [NB, Hkv, bs, d], or all layers at
+    once as [L, NB, Hkv, bs, d]."""
+    lib = load_library()
+    if not isinstance(plan, MovePlan):
+        plan = MovePlan(plan, k_cache.shape[k_cache.dim() - 4])
+    tensors = [k_cache, v_cache] + ([block_tables] if block_tables is not None else [])
+    _check_device(*tensors)
+    need = plan.workspace_size(k_cache, 1, block_tables is not None) if workspace is None else 0
+    workspace, wptr, wbytes = _workspace(need, workspace, k_cache.device, stream)
+    d = [ctypes.byref(describe(x)) for x in tensors]
+    _check(lib.pa_move_blocks(plan._h, d[0], d[1], d[2] if block_tables is not None else None,
+                              wptr, wbytes, _stream_handle(stream)))
 
 
 TIMED_KERNELS = {"decode": 0, "prefill": 1, "shared_prefix": 2}

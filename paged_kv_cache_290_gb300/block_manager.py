@@ -75,6 +75,15 @@ class BlockManager:
     def free(self, seq_id: int) -> None:
         _check(self._lib.pa_bm_free(self._h, int(seq_id)))
 
+    def compact(self, in_order: bool = False) -> List[Tuple[int, int]]:
+        """Renumber the used blocks to the front of the pool (``in_order``: sequence after
+        sequence); returns the (old, new) moves, for ``move_blocks`` before the pool's next use."""
+        moves = (ctypes.c_int32 * (2 * self.num_blocks))()
+        n = ctypes.c_int32(0)
+        _check(self._lib.pa_bm_compact(self._h, int(bool(in_order)), moves, self.num_blocks,
+                                       ctypes.byref(n)))
+        return [(moves[2 * i], moves[2 * i + 1]) for i in range(n.value)]
+
     def stats(self) -> Stats:
         v = [ctypes.c_int32(0) for _ in range(4)]
         _check(self._lib.pa_bm_stats(self._h, *[ctypes.byref(x) for x in v]))

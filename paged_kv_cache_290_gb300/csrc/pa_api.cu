@@ -12,6 +12,7 @@
 
 #include "pa.h"
 #include "pa_common.cuh"
+#include "pa_host.h"
 #include "pa_kernels.h"
 
 static_assert(PA_WAIT_LIMIT_DEFAULT_NS == pa::kWaitLimitNs, "default wait limit");
@@ -23,6 +24,10 @@ thread_local cudaEvent_t g_time_start[3] = {};  // indexed by PA_TIMED_*
 thread_local cudaEvent_t g_time_stop[3] = {};
 thread_local uint64_t g_wait_limit_ns = pa::kWaitLimitNs;  // pa_set_wait_limit
 
+}  // namespace
+
+namespace pa {
+
 int fail(int code, const std::string& msg) {
   g_last_error = msg;
   return code;
@@ -31,6 +36,16 @@ int fail(int code, const std::string& msg) {
 int cuda_fail(cudaError_t e, const char* what) {
   return fail(PA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
+
+void clear_last_error() { g_last_error.clear(); }
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns; }
+
+}  // namespace pa
+
+namespace {
+
+using namespace pa;  // the helpers that pa_host.h declares
 
 // The device error word.  Kernels get its device address; pa_get_device_error reads it.
 __device__ unsigned g_device_error_word;
@@ -86,13 +101,11 @@ cudaError_t error_word_for(void* stream, unsigned** out) {
 // kernels on the caller's stream (fork and join through the events), so the HBM-bound decode
 // grid fills the SMs the compute-bound prefill grid leaves idle in its tail.  Created on first
 // use and kept for the thread's lifetime.
-struct SideStream {
-  cudaStream_t stream = nullptr;
-  cudaEvent_t fork = nullptr, join = nullptr;
-};
 thread_local SideStream g_side[kMaxDevices];
 
-cudaError_t side_stream(SideStream** out) {
+}  // namespace
+
+cudaError_t pa::side_stream(SideStream** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -109,6 +122,8 @@ cudaError_t side_stream(SideStream** out) {
   *out = &s;
   return cudaSuccess;
 }
+
+namespace {
 
 // CTAs per launch of the two-tile prefill kernel beside the decode kernel (0: one full grid).
 // The prefill launches hold whole SMs; the decode kernel streams on the rest.  When the decode
@@ -131,8 +146,10 @@ int prefill_ctas_beside_decode(int num_sms, int64_t decode_rows, int64_t prefill
   return r >= 0.8 ? num_sms * 2 / 3 : 0;
 }
 
+}  // namespace
+
 // SM count of the current device (looked up once per device).
-cudaError_t device_sm_count(int* out) {
+cudaError_t pa::device_sm_count(int* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -145,6 +162,8 @@ cudaError_t device_sm_count(int* out) {
   *out = g_sm_count[dev];
   return cudaSuccess;
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -159,6 +178,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+}  // namespace
+
+namespace pa {
 
 // The pool [NB, Hkv, bs, d] as a 2-D tensor of NB*Hkv*bs rows x d elements, in the layout the
 // kernels' fragment loads expect.  fp16 / bf16: boxes of 16 rows x 64 values (128 bytes),
@@ -192,6 +215,7 @@ const char* dtype_name(int dt) {
     case PA_I64: return "int64";
     case PA_F8E4M3: return "float8_e4m3";
     case PA_BF16: return "bfloat16";
+    case PA_F32: return "float32";
     default: return "unknown";
   }
 }
@@ -236,7 +260,7 @@ int check_contiguous(const pa_tensor* t, const char* name) {
 int pool_dtype16(const pa_tensor* kc) { return kc && kc->dtype == PA_BF16 ? PA_BF16 : PA_F16; }
 
 // Pool [NB, Hkv, bs, d] checks shared by both entry points.
-int check_pool(const pa_tensor* kc, const pa_tensor* vc, int dtype = PA_F16) {
+int check_pool(const pa_tensor* kc, const pa_tensor* vc, int dtype) {
   int rc;
   if ((rc = check_tensor(kc, "k_cache", dtype, 4))) return rc;
   if ((rc = check_tensor(vc, "v_cache", dtype, 4))) return rc;
@@ -258,6 +282,18 @@ int check_pool(const pa_tensor* kc, const pa_tensor* vc, int dtype = PA_F16) {
     return fail(PA_ERR_INVALID_ARG, "k_cache / v_cache must be 16-byte aligned");
   return PA_OK;
 }
+
+int check_scales(const pa_kv_scales* sc) {
+  if (!sc) return fail(PA_ERR_INVALID_ARG, "scales is NULL");
+  for (float x : {sc->k_scale, sc->v_scale})
+    if (!(x > 0.f) || !(x < INFINITY))
+      return fail(PA_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
+  return PA_OK;
+}
+
+}  // namespace pa
+
+namespace {
 
 constexpr size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -293,14 +329,6 @@ int pa_version(void) { return PA_VERSION; }
 size_t pa_attention_workspace_size(int64_t num_tokens, int64_t num_q_heads, int64_t head_dim,
                                    int32_t max_seq_len) {
   return workspace_layout(num_tokens, num_q_heads, head_dim, max_seq_len).total;
-}
-
-static int check_scales(const pa_kv_scales* sc) {
-  if (!sc) return fail(PA_ERR_INVALID_ARG, "scales is NULL");
-  for (float x : {sc->k_scale, sc->v_scale})
-    if (!(x > 0.f) || !(x < INFINITY))
-      return fail(PA_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
-  return PA_OK;
 }
 
 // The scatter-write into an fp16 cache (sc == NULL) or an FP8 cache with scales sc.

@@ -10,6 +10,7 @@
 // chain key, salt and tokens), and its place in the evictable LRU list; per sequence its tokens,
 // block list and the chain keys of its full blocks.  Every entry point first checks that it can
 // finish (arguments, pool capacity), then mutates, so a failing call changes nothing.
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <list>
@@ -309,6 +310,70 @@ int pa_bm_free(pa_block_manager* bm, int64_t seq_id) {
   for (int32_t id : it->second.blocks) bm->release(id);
   bm->seqs.erase(it);
   return ok();
+}
+
+int pa_bm_compact(pa_block_manager* bm, int32_t in_order, int32_t* moves, int32_t max_moves,
+                  int32_t* num_moves) {
+  if (!bm || !num_moves || max_moves < 0 || (max_moves > 0 && !moves))
+    return fail(PA_ERR_INVALID_ARG, "compact: NULL argument or negative size");
+  try {
+    const int32_t nb = bm->num_blocks;
+    std::vector<int32_t> to(static_cast<size_t>(nb), -1);  // new id of every used block
+    int32_t used = 0;
+    if (in_order) {
+      std::vector<int64_t> ids;
+      ids.reserve(bm->seqs.size());
+      for (const auto& kv : bm->seqs) ids.push_back(kv.first);
+      std::sort(ids.begin(), ids.end());
+      for (int64_t id : ids)
+        for (int32_t b : bm->seqs.find(id)->second.blocks)
+          if (to[b] < 0) to[b] = used++;
+      for (int32_t b : bm->lru) to[b] = used++;
+    } else {
+      for (int32_t b = 0; b < nb; ++b)
+        if (bm->blocks[b].ref > 0 || bm->blocks[b].in_lru) ++used;
+      int32_t hole = 0;
+      for (int32_t b = 0; b < nb; ++b) {
+        if (bm->blocks[b].ref == 0 && !bm->blocks[b].in_lru) continue;
+        if (b < used) {
+          to[b] = b;
+          continue;
+        }
+        while (bm->blocks[hole].ref > 0 || bm->blocks[hole].in_lru) ++hole;
+        to[b] = hole++;
+      }
+    }
+    int32_t n = 0;
+    for (int32_t b = 0; b < nb; ++b) n += to[b] >= 0 && to[b] != b;
+    if (n > max_moves)
+      return fail(PA_ERR_INVALID_ARG, "compact: moves holds " + std::to_string(max_moves) +
+                                          " pairs, " + std::to_string(n) + " needed");
+    std::vector<Block> blocks(static_cast<size_t>(nb));
+    std::vector<int32_t> free_list;
+    free_list.reserve(static_cast<size_t>(nb));
+    // from here on nothing allocates: the manager changes as a whole
+    int32_t i = 0;
+    for (int32_t b = 0; b < nb; ++b) {
+      if (to[b] < 0) continue;
+      if (to[b] != b) {
+        moves[2 * i] = b;
+        moves[2 * i + 1] = to[b];
+        ++i;
+      }
+      blocks[to[b]] = std::move(bm->blocks[b]);
+    }
+    for (int32_t b = nb - 1; b >= used; --b) free_list.push_back(b);  // the lowest is taken first
+    bm->blocks.swap(blocks);
+    bm->free_list.swap(free_list);
+    for (int32_t& b : bm->lru) b = to[b];
+    for (auto& kv : bm->cache) kv.second = to[kv.second];
+    for (auto& kv : bm->seqs)
+      for (int32_t& b : kv.second.blocks) b = to[b];
+    *num_moves = n;
+    return ok();
+  } catch (...) {
+    return fail(PA_ERR_INVALID_ARG, "compact: out of host memory");
+  }
 }
 
 int pa_bm_stats(const pa_block_manager* bm, int32_t* free_blocks, int32_t* evictable_blocks,

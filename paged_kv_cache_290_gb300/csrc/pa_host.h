@@ -1,0 +1,46 @@
+// Host-side helpers shared by the C ABI's translation units: status messages, argument checks,
+// tensor maps of the pools, the side stream.  Defined in pa_api.cu.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "pa.h"
+
+namespace pa {
+
+// Sets the message pa_last_error() returns on this host thread; returns `code`.
+int fail(int code, const std::string& msg);
+int cuda_fail(cudaError_t e, const char* what);
+void clear_last_error();
+
+const char* dtype_name(int dt);
+// Rank, dtype, non-negative shape and strides, unit innermost stride, non-null when non-empty.
+int check_tensor(const pa_tensor* t, const char* name, int dtype, int ndim);
+int check_contiguous(const pa_tensor* t, const char* name);
+bool aligned16(const void* p);
+// bfloat16 when the pool says so, else fp16.
+int pool_dtype16(const pa_tensor* kc);
+// Pools [NB, Hkv, bs, d] of the given dtype: shapes, contiguity, supported d and bs, alignment.
+int check_pool(const pa_tensor* kc, const pa_tensor* vc, int dtype);
+int check_scales(const pa_kv_scales* sc);
+
+// The pool as a 2-D tensor map (16-row boxes; see pa_api.cu).
+int make_pool_map(CUtensorMap* m, void* base, int64_t rows, int d, int dtype);
+
+cudaError_t device_sm_count(int* out);
+
+// A side stream and two events per device and host thread, for work beside the caller's stream.
+struct SideStream {
+  cudaStream_t stream = nullptr;
+  cudaEvent_t fork = nullptr, join = nullptr;
+};
+cudaError_t side_stream(SideStream** out);
+
+// The bounded-wait limit of this host thread's calls (pa_set_wait_limit).
+uint64_t wait_limit_ns();
+
+}  // namespace pa

@@ -1,0 +1,337 @@
+// Moves of whole pages inside the pool, in place, where a move's destination may be another
+// move's source (chains and cycles, as a compaction makes them), and the block tables' new ids.
+//
+// Plan (host, once per list of moves).  Moves are put in chain order, each chain from its end:
+// the move out of a page then comes before the move into it.  Consecutive moves form groups of
+// kGroup, and groups form launches of at most kMaxMoves moves.  A thread owns one 16-byte chunk
+// of every page of a group: it loads the chunk of all the group's sources, then stores them to
+// the destinations, so inside a group any chain or cycle is safe.  Launches run one after the
+// other.  What is left is a page that another group overwrites in the same launch, or that an
+// earlier launch has overwritten: those sources (one or two per kGroup moves of a long chain,
+// none where holes are filled) are first copied into the workspace and read from there.
+//
+// Bound by HBM: each moved byte is read and written once, plus staging (at most about 2 in
+// kGroup of the moves).  The moves travel as kernel arguments: no upload, and a captured launch
+// keeps its own copy.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "pa.h"
+#include "pa_common.cuh"
+#include "pa_host.h"
+#include "pa_kernels.h"
+
+namespace pa {
+namespace {
+
+constexpr int kGroup = 8;
+constexpr int kMaxMoves = 1024;  // per launch: 12 KB of the 32 KB of kernel arguments
+constexpr int kThreads = 256;
+static_assert(kMaxMoves % kGroup == 0, "a group lies in one launch");
+
+struct MoveArgs {
+  uint4* k;
+  uint4* v;
+  uint4* stage;          // [slot][layer of the batch][K, V][chunks]
+  int64_t layer_stride;  // chunks between layers of the pools
+  int64_t chunks;        // 16-byte chunks of one page of K (or V)
+  int layer0, layers;    // the batch of layers this launch covers
+  int n;
+  int32_t* old_ids;      // tables: the move's old and new id by position, and a page's position
+  int32_t* new_ids;
+  int32_t* position;
+  int base;              // position of this launch's first move
+  int32_t src[kMaxMoves];  // page id, or ~slot of the workspace
+  int32_t dst[kMaxMoves];  // page id, or ~slot
+  int32_t id[kMaxMoves];   // the moved page's old id
+};
+
+__device__ __forceinline__ uint4 load_once(const uint4* p) { return __ldcs(p); }
+__device__ __forceinline__ void store_once(uint4* p, const uint4& x) { __stcs(p, x); }
+
+__global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ MoveArgs a) {
+  const int g0 = static_cast<int>(blockIdx.y) * kGroup;
+  const int lz = static_cast<int>(blockIdx.z) >> 1, kv = static_cast<int>(blockIdx.z) & 1;
+  if (a.position && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x < kGroup) {
+    const int i = g0 + static_cast<int>(threadIdx.x);
+    if (i < a.n) {
+      a.old_ids[a.base + i] = a.id[i];
+      a.new_ids[a.base + i] = a.dst[i];
+      a.position[a.id[i]] = a.base + i;
+    }
+  }
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (c >= a.chunks) return;
+  uint4* pool = (kv ? a.v : a.k) + (a.layer0 + lz) * a.layer_stride + c;
+  uint4* stage = a.stage + (static_cast<int64_t>(lz) * 2 + kv) * a.chunks + c;
+  const int64_t slot = static_cast<int64_t>(a.layers) * 2 * a.chunks;  // chunks per slot
+  auto at = [&](int32_t i) { return i >= 0 ? pool + i * a.chunks : stage + ~i * slot; };
+  uint4 x[kGroup];
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i)
+    if (g0 + i < a.n) x[i] = load_once(at(a.src[g0 + i]));
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i)
+    if (g0 + i < a.n) store_once(at(a.dst[g0 + i]), x[i]);
+}
+
+// A moved page's id is replaced.  `position` is meaningful for moved pages only: any other entry
+// holds whatever the workspace held, and is told apart by old_ids.
+__global__ void __launch_bounds__(kThreads)
+    rename_kernel(int32_t* tables, int64_t rows, int cols, int64_t stride, int64_t num_blocks, int n,
+                  const int32_t* old_ids, const int32_t* new_ids, const int32_t* position) {
+  const int64_t total = rows * cols;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    int32_t* e = tables + i / cols * stride + i % cols;
+    const int32_t id = *e;
+    if (id < 0 || id >= num_blocks) continue;  // padding
+    const int32_t p = position[id];
+    if (p >= 0 && p < n && old_ids[p] == id) *e = new_ids[p];
+  }
+}
+
+}  // namespace
+}  // namespace pa
+
+struct pa_move_plan {
+  int64_t num_blocks = 0;
+  std::vector<int32_t> src, dst, id;  // the moves in order; src: page, or ~slot
+  std::vector<int32_t> staged;        // page of each workspace slot
+};
+
+namespace {
+
+// Fills `p` from the checked pairs; throws std::bad_alloc.
+void make_plan(pa_move_plan* p, const int32_t* pairs, int64_t n) {
+  const size_t nb = static_cast<size_t>(p->num_blocks);
+  std::vector<int32_t> from(nb, -1), to(nb, -1), order(nb, -1);
+  for (int64_t i = 0; i < n; ++i)
+    if (pairs[2 * i] != pairs[2 * i + 1]) {
+      to[pairs[2 * i]] = pairs[2 * i + 1];
+      from[pairs[2 * i + 1]] = pairs[2 * i];
+    }
+  // the move into page x is recorded at order[x]
+  auto emit = [&](int32_t x) {
+    order[x] = static_cast<int32_t>(p->dst.size());
+    p->id.push_back(from[x]);
+    p->dst.push_back(x);
+  };
+  for (int64_t i = 0; i < n; ++i)  // chains, from the page that nothing leaves
+    if (to[pairs[2 * i + 1]] < 0 && from[pairs[2 * i + 1]] >= 0)
+      for (int32_t x = pairs[2 * i + 1]; x >= 0 && from[x] >= 0; x = from[x]) emit(x);
+  for (int64_t i = 0; i < n; ++i)  // cycles
+    for (int32_t x = pairs[2 * i + 1]; from[x] >= 0 && order[x] < 0; x = from[x]) emit(x);
+  p->src = p->id;
+  for (size_t j = 0; j < p->src.size(); ++j) {
+    const int32_t i = order[p->id[j]];  // the move that overwrites this source
+    if (i < 0 || static_cast<size_t>(i) / pa::kGroup == j / pa::kGroup) continue;
+    if (static_cast<size_t>(i) > j && static_cast<size_t>(i) / pa::kMaxMoves != j / pa::kMaxMoves)
+      continue;  // a later launch
+    p->src[j] = ~static_cast<int32_t>(p->staged.size());
+    p->staged.push_back(p->id[j]);
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t rename_bytes(const pa_move_plan* p) {
+  return 2 * up256(p->dst.size() * sizeof(int32_t)) +
+         up256(static_cast<size_t>(p->num_blocks) * sizeof(int32_t));
+}
+
+// One layer [NB, Hkv, bs, d] of a pool given as such or as [L, NB, Hkv, bs, d].
+int layers_of(const pa_tensor* x, const char* name, pa_tensor* layer, int64_t* num, int64_t* stride) {
+  if (!x) return pa::fail(PA_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (x->ndim != 4 && x->ndim != 5)
+    return pa::fail(PA_ERR_INVALID_ARG, std::string(name) + " must have rank 4 or 5");
+  const int o = x->ndim - 4;
+  *layer = *x;
+  layer->ndim = 4;
+  for (int i = 0; i < 4; ++i) {
+    layer->shape[i] = x->shape[i + o];
+    layer->stride[i] = x->stride[i + o];
+  }
+  *num = o ? x->shape[0] : 1;
+  *stride = o ? x->stride[0] : 0;
+  if (*num < 1 || *num > 32767)
+    return pa::fail(PA_ERR_INVALID_ARG, std::string(name) + " must have 1 to 32767 layers");
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_move_plan* pa_move_plan_create(const int32_t* pairs, int64_t n, int64_t num_blocks) {
+  using namespace pa;
+  clear_last_error();
+  if (n < 0 || (n > 0 && !pairs) || num_blocks < 0 || num_blocks > INT32_MAX) {
+    fail(PA_ERR_INVALID_ARG, "move plan: NULL pairs or bad size");
+    return nullptr;
+  }
+  pa_move_plan* p = nullptr;
+  try {
+    std::vector<uint8_t> seen(static_cast<size_t>(num_blocks), 0);
+    for (int64_t i = 0; i < n; ++i)
+      for (int e = 0; e < 2; ++e) {
+        const int32_t b = pairs[2 * i + e];
+        if (b < 0 || b >= num_blocks) {
+          fail(PA_ERR_INVALID_ARG, "move plan: a block id is outside the pool");
+          return nullptr;
+        }
+        if (seen[b] & (1 << e)) {
+          fail(PA_ERR_INVALID_ARG, e ? "move plan: two moves into one block"
+                                     : "move plan: two moves out of one block");
+          return nullptr;
+        }
+        seen[b] |= 1 << e;
+      }
+    p = new pa_move_plan();
+    p->num_blocks = num_blocks;
+    make_plan(p, pairs, n);
+    return p;
+  } catch (...) {
+    delete p;
+    try {
+      fail(PA_ERR_INVALID_ARG, "move plan: out of host memory");
+    } catch (...) {
+    }
+    return nullptr;
+  }
+}
+
+void pa_move_plan_destroy(pa_move_plan* plan) { delete plan; }
+
+int64_t pa_move_plan_staged(const pa_move_plan* plan) {
+  return plan ? static_cast<int64_t>(plan->staged.size()) : 0;
+}
+
+size_t pa_move_blocks_workspace_size(const pa_move_plan* plan, const pa_tensor* k_cache,
+                                     int32_t layers, int32_t with_tables) {
+  pa_tensor l;
+  int64_t num, stride;
+  if (!plan || layers < 1 || layers_of(k_cache, "k_cache", &l, &num, &stride)) return 0;
+  const size_t page = static_cast<size_t>(l.shape[1] * l.shape[2] * l.shape[3]) *
+                      (l.dtype == PA_F8E4M3 ? 1 : 2);
+  return (with_tables && !plan->dst.empty() ? rename_bytes(plan) : 0) +
+         plan->staged.size() * 2 * page * layers;
+}
+
+int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                   const pa_tensor* block_tables, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  using namespace pa;
+  clear_last_error();
+  if (!plan) return fail(PA_ERR_INVALID_ARG, "plan is NULL");
+  int rc;
+  pa_tensor kl, vl;
+  int64_t layers, vlayers, kstride, vstride;
+  if ((rc = layers_of(k_cache, "k_cache", &kl, &layers, &kstride))) return rc;
+  if ((rc = layers_of(v_cache, "v_cache", &vl, &vlayers, &vstride))) return rc;
+  const bool fp8 = kl.dtype == PA_F8E4M3;
+  if ((rc = check_pool(&kl, &vl, fp8 ? PA_F8E4M3 : pool_dtype16(&kl)))) return rc;
+  if (layers != vlayers || kstride != vstride)
+    return fail(PA_ERR_INVALID_ARG, "k_cache and v_cache layers differ");
+  if (kl.shape[0] != plan->num_blocks)
+    return fail(PA_ERR_INVALID_ARG, "the plan was made for a pool of " +
+                                        std::to_string(plan->num_blocks) + " blocks");
+  const int64_t page = kl.shape[1] * kl.shape[2] * kl.shape[3];  // values
+  const int64_t per16 = fp8 ? 16 : 8;
+  if (layers > 1 && (kstride < kl.shape[0] * page || kstride % per16 != 0))
+    return fail(PA_ERR_INVALID_ARG, "layers must not overlap and must be 16-byte aligned");
+  if (block_tables) {
+    if ((rc = check_tensor(block_tables, "block_tables", PA_I32, 2))) return rc;
+    if (block_tables->shape[1] > INT32_MAX ||
+        (block_tables->shape[0] > 1 && block_tables->stride[0] < block_tables->shape[1]))
+      return fail(PA_ERR_INVALID_ARG, "block_tables row stride must cover its columns");
+  }
+  const int64_t n = static_cast<int64_t>(plan->dst.size());
+  if (n == 0) return PA_OK;
+  // K's and V's layers may alternate in one buffer, but no two may overlap
+  const int64_t k0 = reinterpret_cast<intptr_t>(kl.data), v0 = reinterpret_cast<intptr_t>(vl.data);
+  const int64_t esize = fp8 ? 1 : 2, one = kl.shape[0] * page * esize, step = kstride * esize;
+  const int64_t apart = k0 > v0 ? k0 - v0 : v0 - k0;
+  if (apart < (layers - 1) * step + one) {
+    const int64_t phase = layers > 1 ? apart % step : 0;
+    if (layers == 1 || phase < one || step - phase < one)
+      return fail(PA_ERR_INVALID_ARG, "k_cache and v_cache overlap");
+  }
+
+  const bool tables = block_tables && block_tables->shape[0] > 0 && block_tables->shape[1] > 0;
+  const size_t fixed = tables ? rename_bytes(plan) : 0;
+  const size_t slot = static_cast<size_t>(page) * 2 * (fp8 ? 1 : 2);  // K and V, one layer
+  const size_t per_layer = plan->staged.size() * slot;
+  const size_t need = fixed + per_layer;
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(PA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+      return fail(PA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  }
+  // as many layers at once as the workspace stages (and a grid's z allows)
+  int64_t batch = per_layer ? static_cast<int64_t>((workspace_bytes - fixed) / per_layer) : layers;
+  batch = std::min<int64_t>(std::max<int64_t>(batch, 1), layers);
+  MoveArgs a;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* old_ids = tables ? reinterpret_cast<int32_t*>(ws) : nullptr;
+  int32_t* new_ids = tables ? reinterpret_cast<int32_t*>(ws + up256(n * sizeof(int32_t))) : nullptr;
+  int32_t* position =
+      tables ? reinterpret_cast<int32_t*>(ws + 2 * up256(n * sizeof(int32_t))) : nullptr;
+  a.k = static_cast<uint4*>(kl.data);
+  a.v = static_cast<uint4*>(vl.data);
+  a.stage = reinterpret_cast<uint4*>(ws + fixed);
+  a.layer_stride = kstride / per16;
+  a.chunks = page / per16;
+  a.old_ids = old_ids;
+  a.new_ids = new_ids;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto launch = [&]() {
+    const dim3 grid(static_cast<unsigned>((a.chunks + kThreads - 1) / kThreads),
+                    static_cast<unsigned>((a.n + kGroup - 1) / kGroup),
+                    static_cast<unsigned>(2 * a.layers));
+    move_kernel<<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  };
+  cudaError_t e;
+  for (int64_t l0 = 0; l0 < layers; l0 += batch) {
+    a.layer0 = static_cast<int>(l0);
+    a.layers = static_cast<int>(std::min(batch, layers - l0));
+    a.position = nullptr;
+    const int64_t ns = static_cast<int64_t>(plan->staged.size());
+    for (int64_t b = 0; b < ns; b += kMaxMoves) {
+      a.n = static_cast<int>(std::min<int64_t>(kMaxMoves, ns - b));
+      for (int i = 0; i < a.n; ++i) {
+        a.src[i] = plan->staged[b + i];
+        a.dst[i] = ~static_cast<int32_t>(b + i);
+      }
+      if ((e = launch()) != cudaSuccess) return cuda_fail(e, "move_blocks staging launch");
+    }
+    a.position = l0 == 0 ? position : nullptr;
+    for (int64_t b = 0; b < n; b += kMaxMoves) {
+      a.n = static_cast<int>(std::min<int64_t>(kMaxMoves, n - b));
+      a.base = static_cast<int>(b);
+      std::copy_n(plan->src.data() + b, a.n, a.src);
+      std::copy_n(plan->dst.data() + b, a.n, a.dst);
+      std::copy_n(plan->id.data() + b, a.n, a.id);
+      if ((e = launch()) != cudaSuccess) return cuda_fail(e, "move_blocks launch");
+    }
+  }
+  if (tables) {
+    const int64_t total = block_tables->shape[0] * block_tables->shape[1];
+    const unsigned blocks = static_cast<unsigned>(
+        std::min<int64_t>((total + kThreads - 1) / kThreads, 152 * 8));
+    rename_kernel<<<blocks, kThreads, 0, st>>>(
+        static_cast<int32_t*>(block_tables->data), block_tables->shape[0],
+        static_cast<int>(block_tables->shape[1]), block_tables->stride[0], plan->num_blocks,
+        static_cast<int>(n), old_ids, new_ids, position);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "block table rename launch");
+  }
+  return PA_OK;
+}
+
+}  // extern "C"
