@@ -326,7 +326,7 @@ int pa_rope_and_cache(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v
  *   diff->norm_weight float32 [2d] or NULL.
  *   out              [T, Hq / 2, 2d] of q's type, contiguous.
  *   workspace        device scratch of pa_diff_attention_workspace_size(...) bytes for the same
- *                    number of sequences, heads and hint; 256-byte aligned.
+ *                    tokens (T), sequences (N), heads and hint; 256-byte aligned.
  * Rows of sequences that the device finds invalid are left unwritten and reported, as in
  * pa_attention.  The weights of a row's hidden keys are 0, but a V value of NaN or infinity at a
  * key that some row of the same chunk sees may reach the chunk's other rows (0 * infinity).
@@ -339,7 +339,7 @@ typedef struct pa_diff {
   float out_scale;
 } pa_diff;
 
-size_t pa_diff_attention_workspace_size(int64_t num_seqs, int64_t num_q_heads,
+size_t pa_diff_attention_workspace_size(int64_t num_tokens, int64_t num_seqs, int64_t num_q_heads,
                                         int64_t num_kv_heads, int64_t head_dim,
                                         const pa_batch_hint* hint);
 

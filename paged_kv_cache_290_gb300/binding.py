@@ -146,7 +146,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                 ("pa_rope_and_cache", ctypes.c_int,
                  [P, P, P, P, ctypes.POINTER(PARope), P, P, P, P, S, VP]),
                 ("pa_diff_attention_workspace_size", ctypes.c_size_t,
-                 [I64, I64, I64, I64, ctypes.POINTER(PABatchHint)]),
+                 [I64, I64, I64, I64, I64, ctypes.POINTER(PABatchHint)]),
                 ("pa_diff_attention", ctypes.c_int,
                  [P, P, P, P, P, P, ctypes.c_float, ctypes.POINTER(PADiff), P,
                   ctypes.POINTER(PABatchHint), VP, ctypes.c_size_t, VP]),
@@ -318,12 +318,12 @@ def rope_and_cache(q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping,
     return q_out
 
 
-def diff_attention_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
-                                  head_dim: int, max_query_len: int, max_seq_len: int,
-                                  num_prefill_seqs: int = 0) -> int:
+def diff_attention_workspace_size(num_tokens: int, num_seqs: int, num_q_heads: int,
+                                  num_kv_heads: int, head_dim: int, max_query_len: int,
+                                  max_seq_len: int, num_prefill_seqs: int = 0) -> int:
     hint = PABatchHint(int(max_query_len), int(max_seq_len), int(num_prefill_seqs), 0)
     return int(load_library().pa_diff_attention_workspace_size(
-        num_seqs, num_q_heads, num_kv_heads, head_dim, ctypes.byref(hint)))
+        num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, ctypes.byref(hint)))
 
 
 def diff_attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale: float,
@@ -348,7 +348,7 @@ def diff_attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
     need = 0
     if workspace is None and q.dim() == 3 and k_cache.dim() == 4:
         need = int(lib.pa_diff_attention_workspace_size(
-            seq_lens.numel(), q.shape[1], k_cache.shape[1], q.shape[2], ctypes.byref(hint)))
+            q.shape[0], seq_lens.numel(), q.shape[1], k_cache.shape[1], q.shape[2], ctypes.byref(hint)))
     workspace, wptr, wbytes = _workspace(need, workspace, q.device, stream)
     d = [describe(x) for x in tensors]
     diff = PADiff(ctypes.pointer(d[7]), ctypes.pointer(d[8]) if norm_weight is not None else None,

@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa_gb300.so")
 SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_prefill.cu", "pa_noalloc.cu",
-           "pa_selftest.cu", "pa_block_manager.cpp", "pa_rope.cu", "pa_diff.cu", "pa_move.cu"]
+           "pa_selftest.cu", "pa_block_manager.cpp", "pa_rope.cu", "pa_diff.cu",
+           "pa_diff_chunk.cu", "pa_move.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -29,6 +29,7 @@
 #include <string>
 
 #include "pa.h"
+#include "pa_chunk.cuh"
 #include "pa_common.cuh"
 #include "pa_diff.h"
 #include "pa_host.h"
@@ -55,6 +56,14 @@ struct RowsCfg {
   static constexpr float kRaiseLog2 = 8.f;
   static_assert(kStages >= 2, "stage ring");
 };
+
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 
 // y of one differential head (kV consecutive dims per lane, a warp per head) -> out.
 template <int D, bool BF>
@@ -155,9 +164,19 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
     for (int st = 0; st < C::kStages; ++st) mbar_init(smem_addr(&bars[warp][st]), 1);
     mbar_init_fence();
   }
+  // A partition without a result says so in its cells (l = -1), and the merge leaves such rows.
+  auto cell = [&](int cc, int m) {
+    const int c = col0 + cc;
+    return ((static_cast<int64_t>(s) * a.verify_rows + c / a.group) * a.num_q_heads +
+            2 * (j * a.group + c % a.group) + m) * a.max_parts + part;
+  };
+  auto no_result = [&] {
+    if (nparts > 1 && tid < 2 * my_cols) a.part_l[cell(tid >> 1, tid & 1)] = -1.f;
+  };
   if (__syncthreads_or(bad)) {
     if (tid == 0) atomicOr(a.err, kErrBlockRange);
-    return leave();
+    leave();
+    return no_result();
   }
 
   const int my_n = warp < nunits ? (nunits - warp + C::kWarps - 1) / C::kWarps : 0;
@@ -302,12 +321,14 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
       const float b1 = m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1];
       const float p00 = exp2f(sc[nt][0] - b0), p10 = exp2f(sc[nt][2] - b0);
       const float p01 = exp2f(sc[nt][1] - b1), p11 = exp2f(sc[nt][3] - b1);
-      l_run[nt][0] += p00 + p10;
-      l_run[nt][1] += p01 + p11;
       // P is rounded to the element type for the matrix product: at most 2^-11 (fp16) or 2^-8
-      // (bf16) of each weight, at random over the keys; l keeps the unrounded p
-      pb0[nt] = movmatrix_trans(pack2<BF>(p00, p01));
-      pb1[nt] = movmatrix_trans(pack2<BF>(p10, p11));
+      // (bf16) of each weight.  l sums the rounded weights, so their errors cancel in part.
+      const uint32_t w0 = pack2<BF>(p00, p01), w1 = pack2<BF>(p10, p11);
+      const float2 f0 = unpack2<BF>(w0), f1 = unpack2<BF>(w1);
+      l_run[nt][0] += f0.x + f1.x;
+      l_run[nt][1] += f0.y + f1.y;
+      pb0[nt] = movmatrix_trans(w0);
+      pb1[nt] = movmatrix_trans(w1);
     }
 
     if (nvalid < 16) {  // V rows past the end: p is 0 there, but 0 * NaN is not
@@ -377,7 +398,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
         dst[dt * 16 + gq + 8] = o[nt][dt][2 + e];
       }
     }
-  if (__syncthreads_or(failed_at >= 0)) return;
+  if (__syncthreads_or(failed_at >= 0)) return no_result();
 
   constexpr int kV = 2 * D / 32;  // dims per lane
   for (int cc = warp; cc < my_cols; cc += C::kWarps) {
@@ -406,8 +427,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
 #pragma unroll
       for (int i = 0; i < kV; ++i) y[m][i] *= inv;
       if (nparts > 1) {
-        const int64_t pi = ((static_cast<int64_t>(s) * a.verify_rows + c / a.group) * a.num_q_heads +
-                            2 * head + m) * a.max_parts + part;
+        const int64_t pi = cell(cc, m);
         float* dst = a.part_o + pi * (2 * D) + lane * kV;
 #pragma unroll
         for (int i = 0; i < kV; i += 4)
@@ -429,7 +449,45 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
   }
 }
 
-// One warp per (query row, differential head): joins both maps' partitions, subtracts, finishes.
+// Joins n partials (m in log2 units, l, O / l) of one map of one row; a lane holds kV dims.
+// False when one of them says that it has no result (l < 0).
+template <int kV>
+__device__ __forceinline__ bool join(const float* po, const float* pm, const float* pl, int n,
+                                     int lane, float (&y)[kV]) {
+  float M = -INFINITY;
+  bool lost = false;
+  for (int p = lane; p < n; p += 32) {
+    M = fmaxf(M, pm[p]);
+    lost |= pl[p] < 0.f;
+  }
+  if (__any_sync(0xffffffffu, lost)) return false;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float wsum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) y[i] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < n; ++p) {
+    const float w = exp2f(pm[p] - M) * pl[p];
+    wsum += w;
+    const float* src = po + static_cast<int64_t>(p) * (32 * kV) + lane * kV;
+#pragma unroll
+    for (int i = 0; i < kV; i += 4) {
+      const float4 t = *reinterpret_cast<const float4*>(src + i);
+      y[i] += w * t.x;
+      y[i + 1] += w * t.y;
+      y[i + 2] += w * t.z;
+      y[i + 3] += w * t.w;
+    }
+  }
+  const float inv = 1.f / wsum;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) y[i] *= inv;
+  return true;
+}
+
+// One warp per (query row, differential head) of the rows kernel: joins both maps' partitions,
+// subtracts, finishes.
 template <int D, bool BF>
 __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffArgs a) {
   grid_launch_dependents();
@@ -449,42 +507,58 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffArgs a) {
     return leave();
   grid_dependency_wait();
   const int64_t row = row0 + qi;
+  const int64_t c0 = ((static_cast<int64_t>(s) * a.verify_rows + qi) * a.num_q_heads + 2 * head) *
+                     a.max_parts;
   float y[2][kV];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const int64_t base =
-        ((static_cast<int64_t>(s) * a.verify_rows + qi) * a.num_q_heads + 2 * head + m) *
-        a.max_parts;
-    float M = -INFINITY;
-    for (int p = lane; p < nparts; p += 32) M = fmaxf(M, a.part_m[base + p]);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float wsum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) y[m][i] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < nparts; ++p) {
-      const float w = exp2f(a.part_m[base + p] - M) * a.part_l[base + p];
-      wsum += w;
-      const float* src = a.part_o + (base + p) * (2 * D) + lane * kV;
-#pragma unroll
-      for (int i = 0; i < kV; i += 4) {
-        const float4 t = *reinterpret_cast<const float4*>(src + i);
-        y[m][i] += w * t.x;
-        y[m][i + 1] += w * t.y;
-        y[m][i + 2] += w * t.z;
-        y[m][i + 3] += w * t.w;
-      }
-    }
-    const float inv = 1.f / wsum;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) y[m][i] *= inv;
+    const int64_t c = c0 + m * a.max_parts;
+    if (!join<kV>(a.part_o + c * (2 * D), a.part_m + c, a.part_l + c, nparts, lane, y[m])) return;
   }
   const float lam = __ldg(a.lam + row * a.lam_stride + head);
   float z[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) z[i] = y[0][i] - lam * y[1][i];
   finish_head<D, BF>(a, z, row, head, lane);
+}
+
+// The same for the chunk kernel's partials: grid y = rank of the chunk's sequence, x over its
+// (row, head)s.
+template <int D, bool BF>
+__global__ void __launch_bounds__(128) diff_chunk_merge_kernel(const DiffArgs a) {
+  __shared__ int warp_count[4], chosen_seq;
+  constexpr int kV = 2 * D / 32;
+  const int s = find_prefill_seq<128>(a, warp_count, &chosen_seq, blockIdx.y, false);
+  if (s < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = a.num_q_heads / 2;
+  const int row0 = a.query_start_loc[s], q_len = a.query_start_loc[s + 1] - row0;
+  const int L = a.seq_lens[s];
+  if (q_len > L || (L + a.block_size - 1) / a.block_size > a.max_blocks || row0 < 0 ||
+      row0 + q_len > a.num_tokens || q_len > a.max_query_len || L > a.max_seq_len)
+    return;
+  const int ctx = L - q_len, tile_q = 128 / a.group;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + warp;
+       i < static_cast<int64_t>(q_len) * heads; i += static_cast<int64_t>(gridDim.x) * 4) {
+    const int qi = static_cast<int>(i / heads), head = static_cast<int>(i % heads);
+    const int kend = ctx + min(q_len, (qi / tile_q + 1) * tile_q);
+    const int tiles = (kend + 127) / 128, per = (tiles + a.key_splits - 1) / a.key_splits;
+    const int n = (tiles + per - 1) / per;  // ranges that hold keys
+    const int64_t row = row0 + qi;
+    const int64_t c0 = (row * a.num_q_heads + 2 * head) * a.key_splits;
+    float y[2][kV];
+    bool all = true;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int64_t c = c0 + m * a.key_splits;
+      all = all && join<kV>(a.chunk_o + c * (2 * D), a.chunk_m + c, a.chunk_l + c, n, lane, y[m]);
+    }
+    if (!all) continue;
+    const float lam = __ldg(a.lam + row * a.lam_stride + head);
+    float z[kV];
+#pragma unroll
+    for (int e = 0; e < kV; ++e) z[e] = y[0][e] - lam * y[1][e];
+    finish_head<D, BF>(a, z, row, head, lane);
+  }
 }
 
 template <int D, int BS, int NT, bool BF>
@@ -551,26 +625,65 @@ cudaError_t launch_diff_merge(const DiffArgs& a, cudaStream_t stream) {
                            : cudaLaunchKernelEx(&cfg, diff_merge_kernel<64, false>, a);
 }
 
+cudaError_t launch_diff_chunk_merge(const DiffArgs& a, cudaStream_t stream) {
+  const int64_t work = static_cast<int64_t>(a.max_query_len) * (a.num_q_heads / 2);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((work + 3) / 4, 1 << 20)),
+                  a.prefill_seqs);
+  if (a.bf16)
+    a.head_dim == 128 ? diff_chunk_merge_kernel<128, true><<<grid, 128, 0, stream>>>(a)
+                      : diff_chunk_merge_kernel<64, true><<<grid, 128, 0, stream>>>(a);
+  else
+    a.head_dim == 128 ? diff_chunk_merge_kernel<128, false><<<grid, 128, 0, stream>>>(a)
+                      : diff_chunk_merge_kernel<64, false><<<grid, 128, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
 namespace {
 
-struct DiffLayout {
-  int part_tokens, parts;
-  size_t m_off, l_off, total;
+// How a call is split, from its host-side facts alone, and the workspace that takes.
+struct DiffPlan {
+  bool chunks;       // sequences with several rows go to the chunk kernel
+  bool rows;         // some sequences may go to the rows kernel
+  int rows_per_seq;  // the rows kernel's most rows of a sequence
+  int prefill_seqs;
+  int part_tokens, parts, key_splits;
+  size_t o, m, l, co, cm, cl, total;  // offsets of the regions
 };
 
-// Partials of both maps for `rows` query rows of each of n sequences; nothing when the longest
-// sequence is one partition.
-DiffLayout diff_layout(int64_t n, int64_t rows, int64_t hq, int64_t d, int64_t max_seq_len) {
-  DiffLayout w{};
-  w.part_tokens = 512;
-  w.parts = static_cast<int>(std::max<int64_t>(1, (max_seq_len + w.part_tokens - 1) / w.part_tokens));
-  if (w.parts <= 1 || n <= 0 || rows <= 0) return w;
+DiffPlan diff_plan(int64_t t, int64_t n, int64_t hq, int64_t hkv, int64_t d,
+                   const pa_batch_hint& hint) {
+  DiffPlan p{};
+  const int64_t group = hq / hkv;
+  // Verify rows: up to 8 columns (one column group) of the rows kernel, which reads the keys once
+  const bool verify = hint.max_query_len * group <= 8;
+  p.chunks = hint.max_query_len > 1 && !verify;
+  p.rows = !(p.chunks && hint.num_prefill_seqs >= n);
+  p.rows_per_seq = p.chunks ? 1 : hint.max_query_len;
+  p.prefill_seqs = static_cast<int>(
+      hint.num_prefill_seqs > 0 ? std::min<int64_t>(hint.num_prefill_seqs, n) : n);
+  p.part_tokens = 512;
+  p.parts = static_cast<int>(
+      std::max<int64_t>(1, (hint.max_seq_len + int64_t{p.part_tokens} - 1) / p.part_tokens));
+  p.key_splits = 1;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t cells = static_cast<size_t>(n) * rows * hq * w.parts;
-  w.m_off = up(cells * 2 * d * sizeof(float));
-  w.l_off = w.m_off + up(cells * sizeof(float));
-  w.total = w.l_off + up(cells * sizeof(float));
-  return w;
+  auto region = [&](size_t bytes) {
+    const size_t at = p.total;
+    p.total += up(bytes);
+    return at;
+  };
+  if (p.rows && p.parts > 1) {
+    const size_t cells = static_cast<size_t>(n) * p.rows_per_seq * hq * p.parts;
+    p.o = region(cells * 2 * d * sizeof(float));
+    p.m = region(cells * sizeof(float));
+    p.l = region(cells * sizeof(float));
+  }
+  if (p.chunks) {
+    const size_t cells = static_cast<size_t>(t) * hq * p.key_splits;
+    p.co = region(cells * 2 * d * sizeof(float));
+    p.cm = region(cells * sizeof(float));
+    p.cl = region(cells * sizeof(float));
+  }
+  return p;
 }
 
 }  // namespace
@@ -578,12 +691,13 @@ DiffLayout diff_layout(int64_t n, int64_t rows, int64_t hq, int64_t d, int64_t m
 
 extern "C" {
 
-size_t pa_diff_attention_workspace_size(int64_t num_seqs, int64_t num_q_heads,
+size_t pa_diff_attention_workspace_size(int64_t num_tokens, int64_t num_seqs, int64_t num_q_heads,
                                         int64_t num_kv_heads, int64_t head_dim,
                                         const pa_batch_hint* hint) {
-  if (!hint || num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0) return 0;
-  return pa::diff_layout(num_seqs, hint->max_query_len, num_q_heads, head_dim, hint->max_seq_len)
-      .total;
+  if (!hint || num_tokens <= 0 || num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads < num_kv_heads ||
+      head_dim <= 0 || hint->max_query_len <= 0 || hint->max_seq_len < 0)
+    return 0;
+  return pa::diff_plan(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, *hint).total;
 }
 
 int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
@@ -655,14 +769,14 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   if (!(diff->out_scale - diff->out_scale == 0.f))
     return fail(PA_ERR_INVALID_ARG, "out_scale must be finite");
 
-  const DiffLayout ws = diff_layout(n, hint->max_query_len, hq, d, hint->max_seq_len);
-  if (ws.total > 0) {
-    if (!workspace || workspace_bytes < ws.total)
-      return fail(PA_ERR_WORKSPACE, "workspace needs " + std::to_string(ws.total) + " bytes");
+  if (t == 0 || n == 0 || hint->max_query_len == 0) return PA_OK;
+  const DiffPlan plan = diff_plan(t, n, hq, hkv, d, *hint);
+  if (plan.total > 0) {
+    if (!workspace || workspace_bytes < plan.total)
+      return fail(PA_ERR_WORKSPACE, "workspace needs " + std::to_string(plan.total) + " bytes");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
       return fail(PA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   }
-  if (t == 0 || n == 0 || hint->max_query_len == 0) return PA_OK;
 
   DiffArgs a{};
   a.q = static_cast<const __half*>(q->data);
@@ -673,9 +787,12 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   a.seq_lens = static_cast<const int32_t*>(seq_lens->data);
   a.query_start_loc = static_cast<const int32_t*>(query_start_loc->data);
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
-  a.part_o = ws.total ? reinterpret_cast<float*>(wsb) : nullptr;
-  a.part_m = ws.total ? reinterpret_cast<float*>(wsb + ws.m_off) : nullptr;
-  a.part_l = ws.total ? reinterpret_cast<float*>(wsb + ws.l_off) : nullptr;
+  a.part_o = reinterpret_cast<float*>(wsb + plan.o);
+  a.part_m = reinterpret_cast<float*>(wsb + plan.m);
+  a.part_l = reinterpret_cast<float*>(wsb + plan.l);
+  a.chunk_o = reinterpret_cast<float*>(wsb + plan.co);
+  a.chunk_m = reinterpret_cast<float*>(wsb + plan.cm);
+  a.chunk_l = reinterpret_cast<float*>(wsb + plan.cl);
   a.num_seqs = static_cast<int>(n);
   a.num_tokens = t;
   a.num_q_heads = static_cast<int>(hq);
@@ -686,10 +803,14 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   a.block_size = static_cast<int>(k_cache->shape[2]);
   a.max_blocks = static_cast<int>(block_tables->shape[1]);
   a.num_blocks = k_cache->shape[0];
-  a.part_tokens = ws.part_tokens;
-  a.max_parts = ws.parts;
+  a.part_tokens = plan.part_tokens;
+  a.max_parts = plan.parts;
   a.max_query_len = hint->max_query_len;
-  a.verify_rows = hint->max_query_len;
+  a.max_seq_len = hint->max_seq_len;
+  a.verify_rows = plan.rows_per_seq;
+  a.prefill_seqs = plan.prefill_seqs;
+  a.decode_skipped = plan.rows ? 0 : 1;
+  a.key_splits = plan.key_splits;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.v_scale = 1.f;
   a.bf16 = dt == PA_BF16 ? 1 : 0;
@@ -706,9 +827,40 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   if ((rc = make_pool_map(&kmap, k_cache->data, rows, static_cast<int>(d), dt))) return rc;
   if ((rc = make_pool_map(&vmap, v_cache->data, rows, static_cast<int>(d), dt))) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto chunks = [&](cudaStream_t on) -> int {
+    cudaError_t ce = launch_diff_chunk(a, kmap, vmap, on);
+    if (ce != cudaSuccess) return cuda_fail(ce, "diff chunk launch");
+    ce = launch_diff_chunk_merge(a, on);
+    return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "diff chunk merge launch");
+  };
+  if (!plan.rows) return chunks(st);
+  // Chunks beside rows: the chunks go first, on the side stream, joined back on every path.
+  struct Join {
+    SideStream* side = nullptr;
+    cudaStream_t st = nullptr;
+    cudaError_t done() {
+      if (!side) return cudaSuccess;
+      cudaError_t je = cudaEventRecord(side->join, side->stream);
+      if (je == cudaSuccess) je = cudaStreamWaitEvent(st, side->join, 0);
+      side = nullptr;
+      return je;
+    }
+    ~Join() { done(); }
+  } join;
+  if (plan.chunks) {
+    SideStream* side = nullptr;
+    if ((e = side_stream(&side)) != cudaSuccess) return cuda_fail(e, "side stream");
+    if ((e = cudaEventRecord(side->fork, st)) != cudaSuccess ||
+        (e = cudaStreamWaitEvent(side->stream, side->fork, 0)) != cudaSuccess)
+      return cuda_fail(e, "stream fork");
+    join.side = side;
+    join.st = st;
+    if ((rc = chunks(side->stream))) return rc;
+  }
   if ((e = launch_diff_rows(a, kmap, vmap, st)) != cudaSuccess) return cuda_fail(e, "diff launch");
   if (a.max_parts > 1 && (e = launch_diff_merge(a, st)) != cudaSuccess)
     return cuda_fail(e, "diff merge launch");
+  if ((e = join.done()) != cudaSuccess) return cuda_fail(e, "stream join");
   return PA_OK;
 }
 

@@ -15,10 +15,18 @@ struct DiffArgs : AttnArgs {
   float out_scale;
   int part_tokens;       // keys per split-context partition
   int num_pairs;         // num_kv_heads / 2
+  int max_seq_len;       // the hint's
+  int key_splits;        // ranges of the keys that the chunk kernel's CTAs share out
+  float* chunk_o;        // partials of the chunk kernel: [T, Hq, key_splits, 2 d]
+  float* chunk_m;        // [T, Hq, key_splits], log2 units
+  float* chunk_l;
 };
 
 cudaError_t launch_diff_rows(const DiffArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                              cudaStream_t stream);
 cudaError_t launch_diff_merge(const DiffArgs& a, cudaStream_t stream);
+cudaError_t launch_diff_chunk(const DiffArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              cudaStream_t stream);
+cudaError_t launch_diff_chunk_merge(const DiffArgs& a, cudaStream_t stream);
 
 }  // namespace pa

@@ -147,7 +147,7 @@ def test_replays_in_a_graph_on_another_stream(make):
     lam, weight = lam.cuda(), weight.cuda()
     out = torch.empty((b.num_tokens, 4, 128), dtype=b.q.dtype, device="cuda")
     ws = torch.empty(max(1, pa.diff_attention_workspace_size(
-        b.num_seqs, 8, 4, 64, b.max_query_len, b.max_seq_len, b.num_prefill_seqs)),
+        b.num_tokens, b.num_seqs, 8, 4, 64, b.max_query_len, b.max_seq_len, b.num_prefill_seqs)),
         dtype=torch.uint8, device="cuda")
 
     def call():
@@ -194,9 +194,10 @@ def test_bad_descriptors_leave_rows_alone():
     bad = b.block_tables.clone()
     bad[3, 1] = b.num_blocks
     bad[4, 0] = -1
+    bad[8, 40] = b.num_blocks + 5  # the second of three partitions
     out, (st, bits) = call(bad, b.seq_lens, b.max_seq_len)
     assert st == B.PA_ERR_OUT_OF_RANGE and bits & 4
-    others(out, {3, 4})
+    others(out, {3, 4, 8})
     long = b.seq_lens.clone()
     long[0] = b.block_tables.shape[1] * b.block_size + 1
     long[1] = 0
@@ -206,3 +207,22 @@ def test_bad_descriptors_leave_rows_alone():
     out, (st, bits) = call(b.block_tables, b.seq_lens, 600)
     assert st == B.PA_ERR_DESCRIPTOR and bits & 16
     others(out, {8, 9})  # more than two partitions' keys
+
+
+def test_bad_chunks_leave_their_rows_alone():
+    b = small_mixed(d=64, hq=16, hkv=4, seed=9226)
+    lam, weight = learned(b)
+    ref, bound = diff_attention_ref(b, lam, weight)
+    bad = b.block_tables.clone()
+    bad[6, 5] = -3  # in every tile of the last chunk
+    out = torch.full((b.num_tokens, 8, 128), float("nan"), dtype=b.q.dtype, device="cuda")
+    pa.diff_attention(b.q.cuda(), b.k_cache.cuda(), b.v_cache.cuda(), bad.cuda(), b.seq_lens.cuda(),
+                      b.query_start_loc.cuda(), b.scale, lam.cuda(), out, b.max_query_len,
+                      b.max_seq_len, norm_weight=weight.cuda(),
+                      num_prefill_seqs=b.num_prefill_seqs)
+    st, bits = pa.get_device_error()
+    assert st == B.PA_ERR_OUT_OF_RANGE and bits & 4
+    r0, r1 = b.query_start_loc[6:8].tolist()
+    assert out[r0:r1].isnan().all()
+    keep = [i for i in range(b.num_tokens) if not r0 <= i < r1]
+    check(out[keep], ref[keep], bound[keep])
