@@ -100,6 +100,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
   return false;
 }
 
+// The same for waits that usually last under a microsecond: it polls 64 times (each poll may
+// sleep in hardware) before it first reads the global timer, whose read takes longer than such a
+// wait.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, unsigned* err,
+                                                uint64_t limit_ns = kWaitLimitNs) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, err, limit_ns);
+}
+
 // ---------------------------------------------------------------- programmatic dependent launch
 
 // Wait until the grids this one depends on have completed and their writes are visible

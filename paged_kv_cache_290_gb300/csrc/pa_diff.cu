@@ -677,7 +677,7 @@ DiffPlan diff_plan(int64_t t, int64_t n, int64_t hq, int64_t hkv, int64_t d,
     p.m = region(cells * sizeof(float));
     p.l = region(cells * sizeof(float));
   }
-  if (p.chunks) {
+  if (p.chunks && p.key_splits > 1) {
     const size_t cells = static_cast<size_t>(t) * hq * p.key_splits;
     p.co = region(cells * 2 * d * sizeof(float));
     p.cm = region(cells * sizeof(float));
@@ -761,8 +761,9 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   const pa_tensor* w = diff->norm_weight;
   if (w) {
     if ((rc = check_tensor(w, "norm_weight", PA_F32, 1))) return rc;
-    if (w->shape[0] != 2 * d)
-      return fail(PA_ERR_INVALID_ARG, "norm_weight must have 2 * head_dim values");
+    if (w->shape[0] != 2 * d || !aligned16(w->data))
+      return fail(PA_ERR_INVALID_ARG,
+                  "norm_weight must have 2 * head_dim values and 16-byte alignment");
     if (!(diff->eps >= 0.f && diff->eps < INFINITY))
       return fail(PA_ERR_INVALID_ARG, "eps must be finite and >= 0");
   }
@@ -830,7 +831,7 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   auto chunks = [&](cudaStream_t on) -> int {
     cudaError_t ce = launch_diff_chunk(a, kmap, vmap, on);
     if (ce != cudaSuccess) return cuda_fail(ce, "diff chunk launch");
-    ce = launch_diff_chunk_merge(a, on);
+    if (a.key_splits > 1) ce = launch_diff_chunk_merge(a, on);
     return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "diff chunk merge launch");
   };
   if (!plan.rows) return chunks(st);

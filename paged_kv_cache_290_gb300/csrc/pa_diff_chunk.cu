@@ -1,30 +1,27 @@
 // Differential attention of query chunks on the 5th-generation tensor cores (the mathematics is
 // in pa_diff.cu).
 //
-// Work item = one CTA = (Q tile, softmax map, kv-head pair, sequence, range of the keys).  A Q
-// tile is 128 rows, each a (query token, head of the pair's group) pair.  A map's result is 2d
-// wide: with d = 128 its accumulator takes 256 of TMEM's 512 columns and two 128 x 128 score
-// buffers the rest, so a CTA holds one map; the two maps of a row are two CTAs.  (Both maps in
-// one CTA with half of V's width each would fit too, but every score and exponential would be
-// computed twice: 8 tile products instead of 6 per 128 keys and row tile.)
+// A Q tile is 128 rows, each a (query token, head of the kv-head pair's group) pair; key tiles are
+// 128 keys.  Per softmax map and key tile: S = Q K^T (M 128, N 128, K d), P = 2^(S - m) in the
+// element type, O += P V (M 128, N 2d, K 128), with S, P and O in TMEM (512 columns).
+//   * d = 64 (diff_chunk_both_kernel): a CTA holds both maps: two score buffers, two 128-column
+//     accumulators.  V is loaded once for both, and the CTA finishes its rows alone.
+//   * d = 128 (diff_chunk_map_kernel): one map's accumulator takes 256 columns and its two score
+//     buffers the rest, so a CTA holds one map and a cluster of two CTAs a Q tile; at the end
+//     each CTA sends the other half of its rows' sums through distributed shared memory and
+//     finishes 64 rows.  (Both maps in one CTA with half of V's width each would fit too, but
+//     every score and exponential would be computed twice: 8 tile products instead of 6.)
 //
-// 640 threads:
-//   * warps 16, 17 stream 128-key tiles of K (one head) and V (two heads, 2d columns) through the
-//     block table into rings of 128-byte-swizzled tiles;
-//   * lane 0 of warp 18 issues the MMAs: S(j) = Q K_j^T (M 128, N 128, K d) into buffer j % 2 and
-//     O += P(j) V_j (M 128, N 2d, K 128), P(j) read from TMEM where it overwrote S(j).  Order:
-//     S(0), S(1), then P(j) V_j, S(j + 2): the pipe computes one tile's products while the
-//     other buffer's tile is in softmax;
-//   * warps 0 .. 15 are the softmax: group j % 2 (256 threads) takes key tile j, a thread per
-//     (row, half of the tile's columns).  O has one base m per row for both groups, raised only
-//     when a tile's maximum passes it by more than 2^8 (then O is rescaled in TMEM, after the
-//     P V before): a function of the tiles' maxima alone, so a group needs only the other
-//     group's maxima of the tile before, known before that group's exponentials, and the two
-//     groups' exponentials overlap.
-// The sum l is of the rounded weights that the P V product uses: the rounding of a weight then
-// cancels in part (measured against float64: 1.37 instead of 1.53 times the output's own
-// rounding).
-// Every wait is bounded; V rows past the last visible key are zeroed before their product.
+// 640 threads in both:
+//   * warps 16, 17 stream K and V tiles through the block table into rings of 128-byte-swizzled
+//     tiles;
+//   * lane 0 of warp 18 issues the MMAs, P read from TMEM where it overwrote S: the pipe computes
+//     one score buffer's products while the other buffer is in softmax;
+//   * warps 0 .. 15 are the softmax: 256 threads per score buffer, a thread per (row, half of the
+//     tile's columns).  The base m of a row is raised only when a maximum passes it by more
+//     than 2^8 (then O is rescaled in TMEM).
+// The sum l is of the rounded weights that the P V product uses.  Every wait is bounded; V rows
+// past the last visible key are zeroed before their product.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -37,26 +34,37 @@
 namespace pa {
 namespace {
 
-template <int D>
+// What both kernels share.  Registers: launched at 96 a thread; the producer warpgroup falls to 64
+// and the softmax warps take 104.
 struct ChunkCfg {
   static constexpr int kRows = 128, kKeys = 128;
-  static constexpr int kHalves = D / 64;
-  static constexpr int kTileBytes = kHalves * kKeys * 128;  // 128 rows of one head
-  static constexpr int kQBytes = kTileBytes, kKBytes = kTileBytes, kVBytes = 2 * kTileBytes;
-  static constexpr int kKStages = D == 128 ? 2 : 4, kVStages = D == 128 ? 2 : 4;
-  static constexpr int kSmemBytes = kQBytes + kKStages * kKBytes + kVStages * kVBytes + 1024;
-  static constexpr int kSoftmax = 512, kGroup = 256;
-  static constexpr int kThreads = kSoftmax + 128;
-  // launched at 96 registers a thread; the producer warpgroup falls to 64, softmax takes 104
+  static constexpr int kSoftmax = 512, kGroup = 256, kThreads = kSoftmax + 128;
   static constexpr int kRegsSoftmax = 104, kRegsOther = 64, kLaunchRegs = 96;
   static constexpr uint32_t kTmemCols = 512, kOCol = 256;
   static constexpr float kRescaleLog2 = 8.f;
-  static_assert(kSmemBytes + 2048 <= 232448, "dynamic + static shared memory fit one SM");
   static_assert(kRegsSoftmax * kSoftmax + kRegsOther * 128 <= kLaunchRegs * kThreads,
                 "register split exceeds the launch allocation");
 };
 
-// The sum of the two values that a packed pair holds, per lane of a packed float32 pair.
+struct BothCfg : ChunkCfg {                       // d = 64
+  static constexpr int kTileBytes = 128 * 128;    // 128 rows of one head
+  static constexpr int kStageBytes = 2 * kTileBytes;  // K1 and K2, or the two halves of V
+  static constexpr int kKStages = 2, kVStages = 3;
+  static constexpr int kSmemBytes = 2 * kTileBytes + (kKStages + kVStages) * kStageBytes + 1024;
+  static_assert(kSmemBytes + 3072 <= 232448, "dynamic + static shared memory fit one SM");
+};
+
+struct MapCfg : ChunkCfg {                        // d = 128
+  static constexpr int kTileBytes = 2 * 128 * 128;  // 128 rows of one head
+  static constexpr int kVKeys = 64;               // keys of a V piece
+  static constexpr int kVBytes = 4 * kVKeys * 128;  // both heads
+  static constexpr int kKStages = 2, kVStages = 4;
+  static constexpr int kSmemBytes = kTileBytes + kKStages * kTileBytes + kVStages * kVBytes + 1024;
+  static_assert(kSmemBytes + 2048 <= 232448, "dynamic + static shared memory fit one SM");
+  static_assert(kVStages * kVBytes >= 64 * 2 * 128 * 4, "64 rows of the other map fit V's ring");
+};
+
+// The two values that a packed pair holds, as a packed float32 pair.
 template <bool BF>
 __device__ __forceinline__ uint64_t widen2(uint32_t pk) {
   if constexpr (BF) {
@@ -67,6 +75,12 @@ __device__ __forceinline__ uint64_t widen2(uint32_t pk) {
   }
 }
 
+// One arrival for the whole warp, after every lane's accesses before it.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // x rounded up to a float32 whose low 8 bits are 0 (NaN cannot occur: maxima ignore it).
 __device__ __forceinline__ uint32_t round_up24(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -74,87 +88,301 @@ __device__ __forceinline__ uint32_t round_up24(float x) {
   return u >= 0x7f800000u ? u : (u + 0xffu) & 0xffffff00u;
 }
 
-template <int D, int BS, bool BF>
-__global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
-    diff_chunk_kernel(const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap, const DiffArgs a) {
-  using C = ChunkCfg<D>;
+// The chunk tile of a CTA: its rows and keys.
+struct Tile {
+  int s, row0, q_len, ctx, qbase, tile_q;
+  int kend;        // keys [0, kend) are visible to some row
+  int key_base;    // this CTA's keys: [key_base, key_stop), in ntiles 128-key tiles
+  int key_stop, ntiles;
+};
+
+// Finds and checks the tile; false when the CTA has none (errors are reported).  All threads of
+// the block call it.
+template <int BS, int kThreads>
+__device__ __forceinline__ bool find_tile(const DiffArgs& a, int* warp_count, int* chosen_seq,
+                                          int qt, int z, int split, bool first, bool lead,
+                                          Tile& t) {
+  t.s = find_prefill_seq<kThreads>(a, warp_count, chosen_seq, z, first);
+  if (t.s < 0) return false;
+  t.tile_q = 128 / a.group;
+  t.row0 = a.query_start_loc[t.s];
+  t.q_len = a.query_start_loc[t.s + 1] - t.row0;
+  const int L = a.seq_lens[t.s];
+  if (t.q_len > L || (L + BS - 1) / BS > a.max_blocks || t.row0 < 0 ||
+      t.row0 + t.q_len > a.num_tokens) {
+    if (lead && threadIdx.x == 0) atomicOr(a.err, kErrDescriptor);
+    return false;
+  }
+  if (t.q_len > a.max_query_len || L > a.max_seq_len) {
+    if (lead && threadIdx.x == 0) atomicOr(a.err, kErrHint);
+    return false;
+  }
+  t.qbase = qt * t.tile_q;
+  if (t.qbase >= t.q_len) return false;
+  t.ctx = L - t.q_len;
+  t.kend = t.ctx + min(t.q_len, t.qbase + t.tile_q);
+  const int all_tiles = (t.kend + 127) / 128;
+  const int per = (all_tiles + a.key_splits - 1) / a.key_splits;
+  t.ntiles = min(all_tiles - split * per, per);
+  if (t.ntiles <= 0) return false;
+  t.key_base = split * per * 128;
+  t.key_stop = min(t.kend, t.key_base + t.ntiles * 128);
+  return true;
+}
+
+// Whether a block id of the tile's keys is outside the pool (this thread's share).
+template <int BS, int kThreads>
+__device__ __forceinline__ bool bad_blocks(const DiffArgs& a, const Tile& t) {
+  bool bad = false;
+  for (int i = t.key_base / BS + static_cast<int>(threadIdx.x); i < (t.key_stop + BS - 1) / BS;
+       i += kThreads) {
+    const int32_t blk = a.block_tables[static_cast<int64_t>(t.s) * a.bt_stride + i];
+    bad |= blk < 0 || blk >= a.num_blocks;
+  }
+  return bad;
+}
+
+// A producer warp: streams kPart-key pieces of `heads` heads from head0 on into a ring; lane u
+// fetches unit u (16 keys), whose block id it reads a piece ahead.  Before returning it waits
+// for its last copies, so none lands after the CTA retires.
+template <int D, int BS, int kPart>
+__device__ __forceinline__ void stream_heads(const DiffArgs& a, const Tile& t,
+                                             const CUtensorMap* tm, int head0, int heads,
+                                             int stages, uint64_t* full, uint64_t* empty,
+                                             uint32_t ring) {
+  constexpr int kHalves = D / 64, kUnits = kPart / 16;
+  const int lane = threadIdx.x & 31;
+  const int pieces = (t.key_stop - t.key_base + kPart - 1) / kPart;
+  const int stage_bytes = heads * kHalves * kPart * 128;
+  auto units_of = [&](int j) {
+    return min(kUnits, (t.key_stop - (t.key_base + j * kPart) + 15) >> 4);
+  };
+  auto block_of = [&](int j) {
+    return lane < units_of(j) ? a.block_tables[static_cast<int64_t>(t.s) * a.bt_stride +
+                                               (t.key_base + j * kPart + 16 * lane) / BS]
+                              : 0;
+  };
+  int issued = 0, next = block_of(0);
+  for (int j = 0; j < pieces; ++j) {
+    const int st = j % stages, round = j / stages, blk = next;
+    if (j + 1 < pieces) next = block_of(j + 1);
+    bool ok = true;
+    if (lane == 0 && round > 0)
+      ok = mbar_wait_short(smem_addr(&empty[st]), (round - 1) & 1, a.err, a.wait_limit_ns);
+    if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+    const int units = units_of(j);
+    const uint32_t bar = smem_addr(&full[st]);
+    if (lane == 0) mbar_arrive_expect_tx(bar, units * heads * kHalves * 2048);
+    __syncwarp();
+    if (lane < units) {
+      const int y = (blk * a.num_kv_heads + head0) * BS + (t.key_base + j * kPart + 16 * lane) % BS;
+      const uint32_t dst = ring + st * stage_bytes + lane * 2048;
+      for (int h = 0; h < heads; ++h)
+#pragma unroll
+        for (int c = 0; c < kHalves; ++c)
+          tma_load_2d(dst + (h * kHalves + c) * (kPart * 128), tm, c * 64, y + h * BS, bar);
+    }
+    issued = j + 1;
+  }
+  if (lane == 0)
+    for (int j = max(0, issued - stages); j < issued; ++j)
+      mbar_wait_short(smem_addr(&full[j % stages]), (j / stages) & 1, a.err, a.wait_limit_ns);
+}
+
+// 64 scores of a thread from TMEM, scaled where the scale cannot go into the exponent, masked;
+// returns their maximum.
+__device__ __forceinline__ float load_scores(uint32_t addr, uint32_t (&sv)[2][32], bool prescale,
+                                             float scale_log2, bool masked, int key0, int pos) {
+  tmem_ld32(addr, sv[0]);
+  tmem_ld32(addr + 32, sv[1]);
+  tmem_wait_ld();
+  tmem_regs_ready(sv[0]);
+  tmem_regs_ready(sv[1]);
+  if (prescale || masked) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c) {
+      float v = __uint_as_float(sv[c >> 5][c & 31]);
+      if (prescale) v *= scale_log2;
+      if (masked && key0 + c > pos) v = -INFINITY;
+      sv[c >> 5][c & 31] = __float_as_uint(v);
+    }
+  }
+  float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 64; c += 2)
+    m2[(c >> 1) & 1] = fmax3(m2[(c >> 1) & 1], __uint_as_float(sv[c >> 5][c & 31]),
+                             __uint_as_float(sv[c >> 5][(c & 31) + 1]));
+  return fmaxf(m2[0], m2[1]);
+}
+
+// P = 2^(score mul + neg_m) of the 64 scores -> 32 TMEM columns, two keys each; returns the sum of
+// the rounded weights.
+template <bool BF>
+__device__ __forceinline__ float store_weights(uint32_t addr, const uint32_t (&sv)[2][32],
+                                               float mul, float neg_m) {
+  const uint64_t mul2 = f32x2(mul, mul), negm2 = f32x2(neg_m, neg_m);
+  uint64_t ps2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+#pragma unroll
+  for (int q8 = 0; q8 < 4; ++q8) {
+    uint32_t pk[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int k = q8 * 16 + 2 * c;
+      float x0, x1;
+      f32x2_split(ffma2(f32x2(__uint_as_float(sv[k >> 5][k & 31]),
+                              __uint_as_float(sv[k >> 5][(k & 31) + 1])),
+                        mul2, negm2),
+                  x0, x1);
+      pk[c] = pack2<BF>(ex2_approx(x0), ex2_approx(x1));
+      ps2[c & 1] = fadd2(ps2[c & 1], widen2<BF>(pk[c]));
+    }
+    tmem_st8(addr + q8 * 8, pk);
+  }
+  float s0, s1, s2, s3;
+  f32x2_split(ps2[0], s0, s1);
+  f32x2_split(ps2[1], s2, s3);
+  return (s0 + s1) + (s2 + s3);
+}
+
+// Columns [0, n) at `addr` of this thread's lane times f.
+__device__ __forceinline__ void rescale(uint32_t addr, int n, float f) {
+  for (int c0 = 0; c0 < n; c0 += 16) {
+    uint32_t t[16];
+    tmem_ld16(addr + c0, t);
+    tmem_wait_ld();
+    tmem_regs_ready(t);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) t[c] = __float_as_uint(__uint_as_float(t[c]) * f);
+    tmem_st16(addr + c0, t);
+  }
+}
+
+// n chunks of 16 bytes at `row` of a 128-byte-swizzled tile's rows are cleared (a whole row of
+// each 64-column half, so the swizzle does not matter).
+template <int kHalves, int kPart>
+__device__ __forceinline__ void clear_row(uint32_t row) {
+#pragma unroll
+  for (int c = 0; c < kHalves * 8; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                     row + (c >> 3) * (kPart * 128) + (c & 7) * 16),
+                 "r"(0u)
+                 : "memory");
+}
+
+__device__ __forceinline__ void alloc_tmem(uint32_t* base, uint32_t cols) {  // one warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(base)),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void free_tmem(uint32_t base, uint32_t cols) {  // the same warp
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+               : "memory");
+}
+
+// Four normalised partial sums.
+__device__ __forceinline__ void store4(float* dst, const uint32_t (&t)[32], int c, float inv) {
+  *reinterpret_cast<float4*>(dst) =
+      make_float4(__uint_as_float(t[c]) * inv, __uint_as_float(t[c + 1]) * inv,
+                  __uint_as_float(t[c + 2]) * inv, __uint_as_float(t[c + 3]) * inv);
+}
+
+// o1 - lambda o2, each step rounded on its own: equal maps cancel to 0 at lambda 1.
+__device__ __forceinline__ float difference(float o1, float o2, float lam) {
+  return __fsub_rn(o1, __fmul_rn(lam, o2));
+}
+
+// kCols consecutive columns of a row's y from col0 on -> out, the row's sum of squares known.
+template <int D, bool BF, int kCols>
+__device__ __forceinline__ void finish_columns(const DiffArgs& a, float (&y)[kCols], float sum,
+                                               __half* out, int col0) {
+  float f = a.out_scale;
+  if (a.norm_w) {
+    f *= rsqrtf(sum * (1.f / (2 * D)) + a.eps);
+#pragma unroll
+    for (int c = 0; c < kCols; c += 4) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(a.norm_w + col0 + c));
+      y[c] *= w.x;
+      y[c + 1] *= w.y;
+      y[c + 2] *= w.z;
+      y[c + 3] *= w.w;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kCols; c += 8)
+    *reinterpret_cast<uint4*>(out + col0 + c) =
+        make_uint4(pack2<BF>(y[c] * f, y[c + 1] * f), pack2<BF>(y[c + 2] * f, y[c + 3] * f),
+                   pack2<BF>(y[c + 4] * f, y[c + 5] * f), pack2<BF>(y[c + 6] * f, y[c + 7] * f));
+}
+
+// All 512 softmax threads meet.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 9, 512;" ::: "memory"); }
+
+// All threads of both CTAs of the cluster meet; their shared-memory accesses before are visible
+// after.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address of `addr` (of this CTA's shared memory) in the CTA of cluster rank `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+template <int BS, bool BF>
+__global__ void __launch_bounds__(BothCfg::kThreads, 1)
+    diff_chunk_both_kernel(const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap, const DiffArgs a) {
+  using C = BothCfg;
+  constexpr int D = 64;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t k_full[C::kKStages], k_empty[C::kKStages];
   __shared__ __align__(8) uint64_t v_full[C::kVStages], v_empty[C::kVStages];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], handed[2][4], pv_done, q_full, drain;
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, drain;
   __shared__ uint32_t tmem_base;
   __shared__ int warp_count[C::kThreads / 32];
   __shared__ int chosen_seq, softmax_stop;
-  // [group][half][row]: maximum of the group's latest tile over each half of its columns, in the
-  // scores' own unit, rounded up to the upper 24 bits of its float32 (what shared memory is left)
-  __shared__ uint16_t max_hi[2][2][C::kRows];
-  __shared__ uint8_t max_lo[2][2][C::kRows];
+  __shared__ float half_max[2][2][C::kRows];  // [map][half][row], of the latest tile
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const uint32_t q_s = smem_addr(smem);
-  const uint32_t k_s = q_s + C::kQBytes;
-  const uint32_t v_s = k_s + C::kKStages * C::kKBytes;
+  const uint32_t q_s = smem_addr(smem);  // both maps' Q tiles
+  const uint32_t k_s = q_s + 2 * C::kTileBytes;
+  const uint32_t v_s = k_s + C::kKStages * C::kStageBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const int map = blockIdx.x & 1, pair = blockIdx.y;
-  const int nsplit = a.key_splits;
+  const int pair = blockIdx.y, nsplit = a.key_splits;
   const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
-  const int nq = gridDim.x / 2;
-  const int qt = nq - 1 - static_cast<int>(blockIdx.x) / 2;  // later tiles see more keys: first
-  const int s = find_prefill_seq<C::kThreads>(a, warp_count, &chosen_seq, z,
-                                              blockIdx.x == 0 && pair == 0 && blockIdx.z == 0);
-  if (s < 0) return;
-  const int tile_q = C::kRows / a.group;  // query tokens per tile
-  const int row0 = a.query_start_loc[s];
-  const int q_len = a.query_start_loc[s + 1] - row0;
-  const int L = a.seq_lens[s];
-  const bool lead = blockIdx.x == 0 && split == 0;
-  if (q_len > L || (L + BS - 1) / BS > a.max_blocks || row0 < 0 || row0 + q_len > a.num_tokens) {
-    if (lead && tid == 0) atomicOr(a.err, kErrDescriptor);
+  Tile tile;
+  if (!find_tile<BS, C::kThreads>(a, warp_count, &chosen_seq, gridDim.x - 1 - blockIdx.x, z, split,
+                                  blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
+                                  blockIdx.x == 0 && split == 0, tile))
     return;
-  }
-  if (q_len > a.max_query_len || L > a.max_seq_len) {
-    if (lead && tid == 0) atomicOr(a.err, kErrHint);
-    return;
-  }
-  const int qbase = qt * tile_q;
-  if (qbase >= q_len) return;
-  const int ctx = L - q_len;
-  const int kend = ctx + min(q_len, qbase + tile_q);  // keys [0, kend) are visible to some row
-  const int all_tiles = (kend + C::kKeys - 1) / C::kKeys;
-  const int per = (all_tiles + nsplit - 1) / nsplit;
-  const int tile_first = split * per;
-  const int ntiles = min(all_tiles - tile_first, per);
-  if (ntiles <= 0) return;
-  const int key_base = tile_first * C::kKeys;
-  const int key_stop = min(kend, key_base + ntiles * C::kKeys);
-
-  int bad = 0;
-  for (int i = key_base / BS + tid; i < (key_stop + BS - 1) / BS; i += C::kThreads) {
-    const int32_t blk = a.block_tables[static_cast<int64_t>(s) * a.bt_stride + i];
-    if (blk < 0 || blk >= a.num_blocks) bad = 1;
-  }
-  // A tile without a result says so in its cells (l = -1), and the merge leaves such rows.
-  auto no_result = [&](int row) {
-    if (row < tile_q * a.group && qbase + row / a.group < q_len)
-      a.chunk_l[(static_cast<int64_t>(row0 + qbase + row / a.group) * a.num_q_heads +
-                 2 * (pair * a.group + row % a.group) + map) * nsplit + split] = -1.f;
+  // the cell of a row's partial, when the keys are split
+  auto cell = [&](int row, int map) {
+    return (static_cast<int64_t>(tile.row0 + tile.qbase + row / a.group) * a.num_q_heads +
+            2 * (pair * a.group + row % a.group) + map) * nsplit + split;
   };
-  if (__syncthreads_or(bad)) {
+  auto real_row = [&](int row) {
+    return row < tile.tile_q * a.group && tile.qbase + row / a.group < tile.q_len;
+  };
+  // A range without a result says so (l = -1), and the merge leaves such rows alone.
+  auto no_result = [&](int row, int map) {
+    if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row, map)] = -1.f;
+  };
+  if (__syncthreads_or(bad_blocks<BS, C::kThreads>(a, tile))) {
     if (tid == 0) atomicOr(a.err, kErrBlockRange);
-    if (tid < C::kRows) no_result(tid);
+    if (tid < 2 * C::kRows) no_result(tid >> 1, tid & 1);
     return;
   }
 
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&tmem_base)),
-                 "r"(C::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(smem_addr(&k_full[i]), 1);
@@ -166,11 +394,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
-      mbar_init(smem_addr(&p_full[i]), C::kGroup);
-      for (int k = 0; k < 4; ++k) mbar_init(smem_addr(&handed[i][k]), 64);
+      mbar_init(smem_addr(&p_full[i]), C::kGroup / 32);
     }
-    mbar_init(smem_addr(&pv_done), 1);
-    mbar_init(smem_addr(&q_full), C::kSoftmax);
+    mbar_init(smem_addr(&q_full), C::kSoftmax / 32);
     mbar_init(smem_addr(&drain), 1);
     mbar_init_fence();
     softmax_stop = 0;
@@ -179,112 +405,368 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_base;
+  const int ntiles = tile.ntiles;
 
   constexpr int kKWarp = C::kSoftmax / 32, kVWarp = kKWarp + 1, kMmaWarp = kKWarp + 2;
   if (warp >= kKWarp) {
     // ================================================ producer / MMA warpgroup
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
-    if (warp == kKWarp || warp == kVWarp) {
-      const bool is_v = warp == kVWarp;
-      const CUtensorMap* tm = is_v ? &vmap : &kmap;
-      const int stages = is_v ? C::kVStages : C::kKStages, heads = is_v ? 2 : 1;
-      const int stage_bytes = is_v ? C::kVBytes : C::kKBytes;
-      const int head0 = 2 * pair + (is_v ? 0 : map);
-      uint64_t* full = is_v ? v_full : k_full;
-      uint64_t* empty = is_v ? v_empty : k_empty;
-      const uint32_t ring = is_v ? v_s : k_s;
-      // lane u fetches unit u (16 keys) of a tile; its block id is read a tile ahead
-      auto units_of = [&](int j) {
-        return min(C::kKeys / 16, (key_stop - (key_base + j * C::kKeys) + 15) >> 4);
-      };
-      auto block_of = [&](int j) {
-        return lane < units_of(j) ? a.block_tables[static_cast<int64_t>(s) * a.bt_stride +
-                                                   (key_base + j * C::kKeys + 16 * lane) / BS]
-                                  : 0;
-      };
-      int issued = 0, next = block_of(0);
-      for (int j = 0; j < ntiles; ++j) {
-        const int st = j % stages, round = j / stages, blk = next;
-        if (j + 1 < ntiles) next = block_of(j + 1);
-        bool ok = true;
-        if (lane == 0 && round > 0)
-          ok = mbar_wait(smem_addr(&empty[st]), (round - 1) & 1, a.err, a.wait_limit_ns);
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-        const int units = units_of(j);
-        const uint32_t bar = smem_addr(&full[st]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, units * heads * C::kHalves * 2048);
-        __syncwarp();
-        if (lane < units) {
-          const int y = (blk * a.num_kv_heads + head0) * BS + (key_base + 16 * lane) % BS;
-          const uint32_t dst = ring + st * stage_bytes + lane * 2048;
-          for (int h = 0; h < heads; ++h)
+    if (warp == kKWarp) {
+      stream_heads<D, BS, C::kKeys>(a, tile, &kmap, 2 * pair, 2, C::kKStages, k_full, k_empty, k_s);
+    } else if (warp == kVWarp) {
+      stream_heads<D, BS, C::kKeys>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s);
+    } else if (warp == kMmaWarp && lane == 0) {
+      constexpr uint32_t kIdS = umma_idesc_f16(C::kRows, C::kKeys, 0, 0, BF);
+      constexpr uint32_t kIdO = umma_idesc_f16(C::kRows, 2 * D, 0, 1, BF);
+      auto issue_s = [&](int t, int j) {
+        const uint32_t qb = q_s + t * C::kTileBytes;
+        const uint32_t kb = k_s + (j % C::kKStages) * C::kStageBytes + t * C::kTileBytes;
 #pragma unroll
-            for (int c = 0; c < C::kHalves; ++c)
-              tma_load_2d(dst + (h * C::kHalves + c) * (C::kKeys * 128), tm, c * 64, y + h * BS,
-                          bar);
-        }
-        issued = j + 1;
+        for (int k = 0; k < D / 16; ++k)
+          umma_f16(tmem + t * 128, umma_sdesc(qb + k * 32, 16, 1024),
+                   umma_sdesc(kb + k * 32, 16, 1024), kIdS, k > 0);
+        umma_commit(smem_addr(&s_full[t]));
+      };
+      auto kwait = [&](int j) {
+        const bool ok = mbar_wait_short(smem_addr(&k_full[j % C::kKStages]),
+                                        (j / C::kKStages) & 1, a.err, a.wait_limit_ns);
+        tmem_fence_after_sync();
+        return ok;
+      };
+      bool ok = mbar_wait_short(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) && kwait(0);
+      if (ok) {
+        issue_s(0, 0);
+        issue_s(1, 0);
+        umma_commit(smem_addr(&k_empty[0]));
       }
-      if (lane == 0)  // no copy lands after the CTA retires
-        for (int j = max(0, issued - stages); j < issued; ++j)
-          mbar_wait(smem_addr(&full[j % stages]), (j / stages) & 1, a.err, a.wait_limit_ns);
+      for (int j = 0; ok && j < ntiles; ++j) {
+        const int vst = j % C::kVStages;
+        const uint32_t vb = v_s + vst * C::kStageBytes;
+        ok = mbar_wait_short(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err,
+                             a.wait_limit_ns);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          ok = ok && mbar_wait_short(smem_addr(&p_full[t]), j & 1, a.err, a.wait_limit_ns);
+          if (!ok) break;
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < C::kKeys / 16; ++k)
+            umma_f16_tmem_a(tmem + C::kOCol + t * 128, tmem + t * 128 + k * 8,
+                            umma_sdesc(vb + k * 16 * 128, C::kKeys * 128, 1024), kIdO,
+                            (j > 0 || k > 0));
+          if (t == 1) umma_commit(smem_addr(&v_empty[vst]));
+          if (j + 1 < ntiles) {
+            if (t == 0) ok = kwait(j + 1);
+            if (ok) issue_s(t, j + 1);
+          }
+        }
+        if (ok && j + 1 < ntiles) umma_commit(smem_addr(&k_empty[(j + 1) % C::kKStages]));
+      }
+      umma_commit(smem_addr(&drain));
+      mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
+    }
+  } else {
+    // ================================================ softmax: 256 threads per map
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    const int g = warp >> 3, h = (warp >> 2) & 1, quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // TMEM lane = row of the tile
+    const uint32_t pair_bar = 1 + g * 4 + quarter;
+    const bool rv = real_row(r);
+    const int tok = tile.qbase + (rv ? r / a.group : 0);
+    const int head = pair * a.group + r % a.group;
+    const int pos = tile.ctx + tok;  // padding rows mirror the tile's first row
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t sbuf = tmem + lane_addr + g * 128;
+    const uint32_t obuf = tmem + lane_addr + C::kOCol;
+
+    {  // half of the Q row of map g -> shared memory, 128B-swizzled K-major
+      const __half* qrow = a.q + static_cast<int64_t>(tile.row0 + tok) * a.q_stride +
+                           static_cast<int64_t>(2 * head + g) * D;
+#pragma unroll
+      for (int cc = 0; cc < D / 16; ++cc) {
+        const int c = h * (D / 16) + cc;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (rv) v = __ldg(reinterpret_cast<const uint4*>(qrow + c * 8));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         q_s + g * C::kTileBytes + swz128(r, c)),
+                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+      }
+      fence_proxy_async();
+      warp_arrive(smem_addr(&q_full));
+    }
+
+    bool stopped = false;
+    float m_run = -INFINITY, l_run = 0.f;  // m in the scores' unit
+    const bool prescale = !(a.scale_log2 > 0.f);
+    const float mul = prescale ? 1.f : a.scale_log2;
+    for (int j = 0; j < ntiles; ++j) {
+      // S(j) of this map done; it was issued after P V of tile j - 1, so O is settled too
+      const bool got = __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&s_full[g]), j & 1, a.err,
+                                                               a.wait_limit_ns));
+      uint32_t sv[2][32];
+      float mloc = -INFINITY;
+      const int key0 = tile.key_base + j * C::kKeys + h * 64;
+      if (got) {
+        tmem_fence_after_sync();
+        mloc = load_scores(sbuf + h * 64, sv, prescale, a.scale_log2,
+                           key0 + 63 > tile.ctx + tile.qbase, key0, pos);
+      }
+      half_max[g][h][r] = mloc;
+      tmem_fence_before_sync();
+      // both halves have read their scores before either stores P over them
+      if (bar_sync_or(pair_bar, 64, !got)) {
+        stopped = true;
+        break;
+      }
+      tmem_fence_after_sync();
+      const float mx = fmaxf(half_max[g][0][r], half_max[g][1][r]);
+      float alpha = 1.f;
+      if ((mx - m_run) * mul > C::kRescaleLog2 || (m_run == -INFINITY && mx > -INFINITY)) {
+        alpha = ex2_approx((m_run - mx) * mul);  // 0 when m_run is still -inf
+        m_run = mx;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f))
+        rescale(obuf + g * 128 + h * D, D, alpha);
+      l_run = l_run * alpha + store_weights<BF>(sbuf + h * 32, sv, mul,
+                                                m_run == -INFINITY ? 0.f : -m_run * mul);
+      const int tile0 = tile.key_base + j * C::kKeys;
+      if (g == 0 && j == ntiles - 1 && tile0 + C::kKeys > tile.key_stop) {
+        // V rows past the last visible key may hold any bits: map 0, whose P V comes first,
+        // clears them once the tile has landed (row r of head h per thread)
+        const int vst = j % C::kVStages;
+        if (!mbar_wait_short(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err,
+                             a.wait_limit_ns))
+          stopped = true;
+        else if (tile0 + r >= tile.key_stop)
+          clear_row<1, C::kKeys>(v_s + vst * C::kStageBytes + h * C::kTileBytes + r * 128);
+        fence_proxy_async();
+      }
+      tmem_wait_st();
+      tmem_fence_before_sync();
+      // a warp that gave up hands over nothing; its pair leaves at the next tile's meeting
+      if (!__any_sync(0xffffffffu, stopped)) warp_arrive(smem_addr(&p_full[g]));
+    }
+
+    // ---- the row's sums of both maps; every softmax thread meets here
+    bool ok = !stopped;
+    if (ok) ok = mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
+    float* red = reinterpret_cast<float*>(smem);  // Q and the rings are done once drained
+    if (!ok) softmax_stop = 1;
+    softmax_sync();
+    ok = !*reinterpret_cast<volatile int*>(&softmax_stop);
+    if (ok) red[(g * 2 + h) * C::kRows + r] = l_run;
+    softmax_sync();
+    if (!ok) {
+      if (h == 0) no_result(r, g);
+    } else {
+      tmem_fence_after_sync();
+      float inv[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float l = red[2 * m * C::kRows + r] + red[(2 * m + 1) * C::kRows + r];
+        inv[m] = l > 0.f ? 1.f / l : 0.f;  // 0: the row sees no key of this range
+        if (nsplit > 1 && rv && h == 0 && g == m) {
+          a.chunk_m[cell(r, m)] = m_run * mul;
+          a.chunk_l[cell(r, m)] = l;
+        }
+      }
+      constexpr int kCols = 2 * D / 4;  // this thread's columns of y
+      const int col0 = (g * 2 + h) * kCols;
+      uint32_t o0[kCols], o1[kCols];
+      tmem_ld32(obuf + col0, o0);
+      tmem_ld32(obuf + 128 + col0, o1);
+      tmem_wait_ld();
+      tmem_regs_ready(o0);
+      tmem_regs_ready(o1);
+      if (nsplit > 1) {
+        if (rv) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            store4(a.chunk_o + cell(r, 0) * (2 * D) + col0 + c, o0, c, inv[0]);
+            store4(a.chunk_o + cell(r, 1) * (2 * D) + col0 + c, o1, c, inv[1]);
+          }
+        }
+      } else {
+        const int64_t row = tile.row0 + tok;
+        const float lam = __ldg(a.lam + row * a.lam_stride + head);
+        float y[kCols], ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          y[c] = difference(__fmul_rn(__uint_as_float(o0[c]), inv[0]),
+                            __fmul_rn(__uint_as_float(o1[c]), inv[1]), lam);
+          ss += y[c] * y[c];
+        }
+        float* sq = red + 4 * C::kRows;
+        sq[(g * 2 + h) * C::kRows + r] = ss;
+        softmax_sync();
+        const float sum = (sq[r] + sq[C::kRows + r]) + (sq[2 * C::kRows + r] + sq[3 * C::kRows + r]);
+        if (rv)
+          finish_columns<D, BF, kCols>(a, y, sum,
+                                       a.out + (row * (a.num_q_heads / 2) + head) * (2 * D), col0);
+      }
+    }
+  }
+
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 0) free_tmem(tmem, C::kTmemCols);
+}
+
+// d = 128: the CTAs of a cluster are the two maps of one Q tile.
+template <int BS, bool BF>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
+    diff_chunk_map_kernel(const __grid_constant__ CUtensorMap kmap,
+                          const __grid_constant__ CUtensorMap vmap, const DiffArgs a) {
+  using C = MapCfg;
+  constexpr int D = 128;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t k_full[C::kKStages], k_empty[C::kKStages];
+  __shared__ __align__(8) uint64_t v_full[C::kVStages], v_empty[C::kVStages];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], handed[2][4], pv_done, q_full, drain;
+  __shared__ uint32_t tmem_base;
+  __shared__ int warp_count[C::kThreads / 32];
+  __shared__ int chosen_seq, softmax_stop, peer_stop;
+  // [group][half][row]: maximum of the group's latest tile over each half of its columns, in the
+  // scores' own unit, rounded up to the upper 24 bits of its float32 (what shared memory is left)
+  __shared__ uint16_t max_hi[2][2][C::kRows];
+  __shared__ uint8_t max_lo[2][2][C::kRows];
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t q_s = smem_addr(smem);
+  const uint32_t k_s = q_s + C::kTileBytes;
+  const uint32_t v_s = k_s + C::kKStages * C::kTileBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int map = blockIdx.x & 1, pair = blockIdx.y, nsplit = a.key_splits;  // map = cluster rank
+  const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
+  Tile tile;
+  // both CTAs of the cluster see the same tile: they leave early together or not at all
+  if (!find_tile<BS, C::kThreads>(a, warp_count, &chosen_seq,
+                                  (gridDim.x - 1 - blockIdx.x) / 2, z, split,
+                                  blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
+                                  blockIdx.x == 0 && split == 0, tile))
+    return;
+  auto cell = [&](int row) {
+    return (static_cast<int64_t>(tile.row0 + tile.qbase + row / a.group) * a.num_q_heads +
+            2 * (pair * a.group + row % a.group) + map) * nsplit + split;
+  };
+  auto real_row = [&](int row) {
+    return row < tile.tile_q * a.group && tile.qbase + row / a.group < tile.q_len;
+  };
+  auto no_result = [&](int row) {
+    if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row)] = -1.f;
+  };
+  if (__syncthreads_or(bad_blocks<BS, C::kThreads>(a, tile))) {
+    if (tid == 0) atomicOr(a.err, kErrBlockRange);
+    if (tid < C::kRows) no_result(tid);
+    return;
+  }
+
+  if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
+  if (tid == 0) {
+    for (int i = 0; i < C::kKStages; ++i) {
+      mbar_init(smem_addr(&k_full[i]), 1);
+      mbar_init(smem_addr(&k_empty[i]), 1);
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
+      mbar_init(smem_addr(&v_full[i]), 1);
+      mbar_init(smem_addr(&v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&s_full[i]), 1);
+      mbar_init(smem_addr(&p_full[i]), C::kGroup / 32);
+      for (int k = 0; k < 4; ++k) mbar_init(smem_addr(&handed[i][k]), 2);
+    }
+    mbar_init(smem_addr(&pv_done), 1);
+    mbar_init(smem_addr(&q_full), C::kSoftmax / 32);
+    mbar_init(smem_addr(&drain), 1);
+    mbar_init_fence();
+    softmax_stop = 0;
+    peer_stop = 1;  // until the peer says otherwise
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tmem = tmem_base;
+  const int ntiles = tile.ntiles;
+  const int pieces = (tile.key_stop - tile.key_base + C::kVKeys - 1) / C::kVKeys;
+
+  constexpr int kKWarp = C::kSoftmax / 32, kVWarp = kKWarp + 1, kMmaWarp = kKWarp + 2;
+  if (warp >= kKWarp) {
+    // ================================================ producer / MMA warpgroup
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
+    if (warp == kKWarp) {
+      stream_heads<D, BS, C::kKeys>(a, tile, &kmap, 2 * pair + map, 1, C::kKStages, k_full,
+                                    k_empty, k_s);
+    } else if (warp == kVWarp) {
+      // V in pieces of 64 keys: a piece's stage is refilled as soon as its half of P V is done
+      stream_heads<D, BS, C::kVKeys>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty,
+                                     v_s);
     } else if (warp == kMmaWarp && lane == 0) {
       constexpr uint32_t kIdS = umma_idesc_f16(C::kRows, C::kKeys, 0, 0, BF);
       constexpr uint32_t kIdO = umma_idesc_f16(C::kRows, 2 * D, 0, 1, BF);
       auto issue_s = [&](int j) {
         const int st = j % C::kKStages;
-        if (!mbar_wait(smem_addr(&k_full[st]), (j / C::kKStages) & 1, a.err, a.wait_limit_ns))
+        if (!mbar_wait_short(smem_addr(&k_full[st]), (j / C::kKStages) & 1, a.err,
+                             a.wait_limit_ns))
           return false;
         tmem_fence_after_sync();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * (C::kKeys * 128) + (k & 3) * 32;
           umma_f16(tmem + (j & 1) * 128, umma_sdesc(q_s + off, 16, 1024),
-                   umma_sdesc(k_s + st * C::kKBytes + off, 16, 1024), kIdS, k > 0);
+                   umma_sdesc(k_s + st * C::kTileBytes + off, 16, 1024), kIdS, k > 0);
         }
         umma_commit(smem_addr(&s_full[j & 1]));
         umma_commit(smem_addr(&k_empty[st]));
         return true;
       };
-      bool ok = mbar_wait(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) && issue_s(0) &&
+      bool ok = mbar_wait_short(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) && issue_s(0) &&
                 (ntiles < 2 || issue_s(1));
       for (int j = 0; ok && j < ntiles; ++j) {
-        const int vst = j % C::kVStages;
-        ok = mbar_wait(smem_addr(&p_full[j & 1]), (j >> 1) & 1, a.err, a.wait_limit_ns) &&
-             mbar_wait(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err, a.wait_limit_ns);
-        if (!ok) break;
-        tmem_fence_after_sync();
-        const uint32_t vb = v_s + vst * C::kVBytes;
+        ok = mbar_wait_short(smem_addr(&p_full[j & 1]), (j >> 1) & 1, a.err, a.wait_limit_ns);
+        // a last tile of at most 64 keys has one piece: the other half of P is 0
+        for (int p = 2 * j; ok && p < min(2 * j + 2, pieces); ++p) {
+          const int vst = p % C::kVStages;
+          ok = mbar_wait_short(smem_addr(&v_full[vst]), (p / C::kVStages) & 1, a.err,
+                               a.wait_limit_ns);
+          if (!ok) break;
+          tmem_fence_after_sync();
+          const uint32_t vb = v_s + vst * C::kVBytes;
 #pragma unroll
-        for (int k = 0; k < C::kKeys / 16; ++k)
-          umma_f16_tmem_a(tmem + C::kOCol, tmem + (j & 1) * 128 + k * 8,
-                          umma_sdesc(vb + k * 16 * 128, C::kKeys * 128, 1024), kIdO,
-                          (j > 0 || k > 0));
-        umma_commit(smem_addr(&v_empty[vst]));
+          for (int k = 0; k < C::kVKeys / 16; ++k)
+            umma_f16_tmem_a(tmem + C::kOCol,
+                            tmem + (j & 1) * 128 + ((p & 1) * (C::kVKeys / 16) + k) * 8,
+                            umma_sdesc(vb + k * 16 * 128, C::kVKeys * 128, 1024), kIdO,
+                            (p > 0 || k > 0));
+          umma_commit(smem_addr(&v_empty[vst]));
+        }
+        if (!ok) break;
         umma_commit(smem_addr(&pv_done));
         if (j + 2 < ntiles) ok = issue_s(j + 2);
       }
       umma_commit(smem_addr(&drain));
-      mbar_wait(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
+      mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
     }
   } else {
-    // ================================================ softmax
+    // ================================================ softmax: group g takes key tiles g, g + 2, ...
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    constexpr int kHalfKeys = C::kKeys / 2;
     const int g = warp >> 3, h = (warp >> 2) & 1, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // TMEM lane = row of the tile
     const uint32_t pair_bar = 1 + g * 4 + quarter;
-    const int qi = r / a.group, hg = r % a.group;
-    const int tok = qbase + qi;
-    const bool rv = qi < tile_q && tok < q_len;
-    const int pos = ctx + (rv ? tok : qbase);  // padding rows mirror the tile's first row
-    const int head = pair * a.group + hg;      // differential head
+    const bool rv = real_row(r);
+    const int tok = tile.qbase + (rv ? r / a.group : 0);
+    const int head = pair * a.group + r % a.group;
+    const int pos = tile.ctx + tok;  // padding rows mirror the tile's first row
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t sbuf = tmem + lane_addr + g * 128;
     const uint32_t obuf = tmem + lane_addr + C::kOCol;
 
     {  // a quarter of the Q row -> shared memory, 128B-swizzled K-major
-      const __half* qrow = a.q + static_cast<int64_t>(row0 + (rv ? tok : 0)) * a.q_stride +
+      const __half* qrow = a.q + static_cast<int64_t>(tile.row0 + tok) * a.q_stride +
                            static_cast<int64_t>(2 * head + map) * D;
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
@@ -297,78 +779,57 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
                      : "memory");
       }
       fence_proxy_async();
-      mbar_arrive(smem_addr(&q_full));
+      warp_arrive(smem_addr(&q_full));
     }
 
     bool stopped = false;
     float m_run = -INFINITY, l_run = 0.f;  // m in the scores' unit
-    const int min_pos = ctx + qbase;
     const bool prescale = !(a.scale_log2 > 0.f);
-    const float mul = prescale ? 1.f : a.scale_log2;  // exponent = fma(score, mul, -m mul)
+    const float mul = prescale ? 1.f : a.scale_log2;
+    auto row_max = [&](int gg) {
+      auto at = [&](int hh) {
+        return __uint_as_float(static_cast<uint32_t>(max_hi[gg][hh][r]) << 16 |
+                               static_cast<uint32_t>(max_lo[gg][hh][r]) << 8);
+      };
+      return fmaxf(at(0), at(1));
+    };
+    auto raises = [&](float m, float x) {
+      return (x - m) * mul > C::kRescaleLog2 || (m == -INFINITY && x > -INFINITY);
+    };
     for (int j = g; j < ntiles; j += 2) {
-      const bool got = __all_sync(
-          0xffffffffu, mbar_wait(smem_addr(&s_full[g]), (j >> 1) & 1, a.err, a.wait_limit_ns));
+      const bool got = __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&s_full[g]), (j >> 1) & 1,
+                                                               a.err, a.wait_limit_ns));
       uint32_t sv[2][32];
       float mloc = -INFINITY;
-      const int key0 = key_base + j * C::kKeys + h * kHalfKeys;
+      const int key0 = tile.key_base + j * C::kKeys + h * 64;
       if (got) {
         tmem_fence_after_sync();
-        tmem_ld32(sbuf + h * kHalfKeys, sv[0]);
-        tmem_ld32(sbuf + h * kHalfKeys + 32, sv[1]);
-        tmem_wait_ld();
-        tmem_regs_ready(sv[0]);
-        tmem_regs_ready(sv[1]);
-        const bool masked = key0 + kHalfKeys - 1 > min_pos;
-        if (prescale || masked) {
-#pragma unroll
-          for (int c = 0; c < kHalfKeys; ++c) {
-            float v = __uint_as_float(sv[c >> 5][c & 31]);
-            if (prescale) v *= a.scale_log2;
-            if (masked && key0 + c > pos) v = -INFINITY;
-            sv[c >> 5][c & 31] = __float_as_uint(v);
-          }
-        }
-        float m2[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kHalfKeys; c += 2)
-          m2[(c >> 1) & 1] = fmax3(m2[(c >> 1) & 1], __uint_as_float(sv[c >> 5][c & 31]),
-                                   __uint_as_float(sv[c >> 5][(c & 31) + 1]));
-        mloc = fmaxf(m2[0], m2[1]);
+        mloc = load_scores(sbuf + h * 64, sv, prescale, a.scale_log2,
+                           key0 + 63 > tile.ctx + tile.qbase, key0, pos);
       }
-      // The other group's maxima of tile j - 1 (its threads wait for this read, through `handed`,
-      // before they store those of tile j + 1).
-      auto row_max = [&](int gg) {
-        auto at = [&](int hh) {
-          return __uint_as_float(static_cast<uint32_t>(max_hi[gg][hh][r]) << 16 |
-                                 static_cast<uint32_t>(max_lo[gg][hh][r]) << 8);
-        };
-        return fmaxf(at(0), at(1));
-      };
+      // The other group's maxima of tile j - 1; its threads wait for this read, through `handed`,
+      // before they store those of tile j + 1.
       float before = -INFINITY;
       if (j > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&handed[g ^ 1][quarter]),
-                                               ((j - 1) >> 1) & 1, a.err, a.wait_limit_ns)))
+        if (!__all_sync(0xffffffffu, mbar_wait_short(smem_addr(&handed[g ^ 1][quarter]),
+                                                     ((j - 1) >> 1) & 1, a.err, a.wait_limit_ns)))
           stopped = true;  // nothing more is written; the pair leaves together below
         before = row_max(g ^ 1);
       }
       const uint32_t up = round_up24(mloc);
       max_hi[g][h][r] = static_cast<uint16_t>(up >> 16);
       max_lo[g][h][r] = static_cast<uint8_t>(up >> 8);
-      // Both halves read the same stored maxima, so they take the same base; and both have read
-      // their scores before either stores P over them.
       tmem_fence_before_sync();
+      // both halves have read their scores before either stores P over them
       if (bar_sync_or(pair_bar, 64, !got || stopped)) {
         stopped = true;
         break;
       }
       tmem_fence_after_sync();
       const float mx = row_max(g);
-      mbar_arrive(smem_addr(&handed[g][quarter]));
+      warp_arrive(smem_addr(&handed[g][quarter]));
       // The base is a function of the maxima so far, so every thread of the row computes the same
       // one: after tile j - 1 (the other group's), then after tile j.
-      auto raises = [&](float m, float x) {
-        return (x - m) * mul > C::kRescaleLog2 || (m == -INFINITY && x > -INFINITY);
-      };
       const float m_prev = j > 0 && raises(m_run, before) ? before : m_run;
       float m_new = m_prev, alpha = 1.f;
       if (raises(m_prev, mx)) {
@@ -377,116 +838,162 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
         // rare: O so far, its last product done, goes over to the new base
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_addr(&pv_done), (j - 1) & 1, a.err,
-                                               a.wait_limit_ns)))
+        if (!__all_sync(0xffffffffu, mbar_wait_short(smem_addr(&pv_done), (j - 1) & 1, a.err,
+                                                     a.wait_limit_ns)))
           stopped = true;
         tmem_fence_after_sync();
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 16) {
-          uint32_t t[16];
-          tmem_ld16(obuf + h * D + c0, t);
-          tmem_wait_ld();
-          tmem_regs_ready(t);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) t[c] = __float_as_uint(__uint_as_float(t[c]) * alpha);
-          tmem_st16(obuf + h * D + c0, t);
-        }
+        rescale(obuf + h * D, D, alpha);
       }
       // this thread's sum is still against its group's base of two tiles ago
       if (m_new != m_run) l_run *= ex2_approx((m_run - m_new) * mul);
       m_run = m_new;
+      l_run += store_weights<BF>(sbuf + h * 32, sv, mul, m_run == -INFINITY ? 0.f : -m_run * mul);
 
-      const float neg_m = m_run == -INFINITY ? 0.f : -m_run * mul;
-      const uint64_t mul2 = f32x2(mul, mul), negm2 = f32x2(neg_m, neg_m);
-      uint64_t ps2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-#pragma unroll
-      for (int q8 = 0; q8 < kHalfKeys / 16; ++q8) {
-        uint32_t pk[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int k = q8 * 16 + 2 * c;
-          float x0, x1;
-          f32x2_split(ffma2(f32x2(__uint_as_float(sv[k >> 5][k & 31]),
-                                  __uint_as_float(sv[k >> 5][(k & 31) + 1])),
-                            mul2, negm2),
-                      x0, x1);
-          pk[c] = pack2<BF>(ex2_approx(x0), ex2_approx(x1));
-          ps2[c & 1] = fadd2(ps2[c & 1], widen2<BF>(pk[c]));
-        }
-        tmem_st8(sbuf + h * (kHalfKeys / 2) + q8 * 8, pk);
-      }
-      float s0, s1, s2, s3;
-      f32x2_split(ps2[0], s0, s1);
-      f32x2_split(ps2[1], s2, s3);
-      l_run += (s0 + s1) + (s2 + s3);
-
-      const int tile0 = key_base + j * C::kKeys;
-      if (j == ntiles - 1 && tile0 + C::kKeys > key_stop) {
-        // V rows past the last visible key may hold any bits: the thread of (row, half) clears
-        // that row of V head h once the tile has landed
-        const int vst = j % C::kVStages;
-        const bool landed =
-            mbar_wait(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err, a.wait_limit_ns);
-        if (landed && tile0 + r >= key_stop) {
-          const uint32_t vrow = v_s + vst * C::kVBytes + h * C::kTileBytes + r * 128;
-#pragma unroll
-          for (int c = 0; c < C::kHalves * 8; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             vrow + (c >> 3) * (C::kKeys * 128) + (c & 7) * 16),
-                         "r"(0u)
-                         : "memory");
-        }
+      const int last = pieces - 1, piece0 = tile.key_base + last * C::kVKeys;
+      if (j == ntiles - 1 && piece0 + C::kVKeys > tile.key_stop) {
+        // V rows past the last visible key may hold any bits: each thread clears half a row of
+        // head h in the last piece once that has landed
+        const int vst = last % C::kVStages, rr = r & (C::kVKeys - 1);
+        if (!mbar_wait_short(smem_addr(&v_full[vst]), (last / C::kVStages) & 1, a.err,
+                             a.wait_limit_ns))
+          stopped = true;
+        else if (piece0 + rr >= tile.key_stop)
+          clear_row<1, C::kVKeys>(v_s + vst * C::kVBytes + (h * 2 + (r >> 6)) * (C::kVKeys * 128) +
+                                  rr * 128);
         fence_proxy_async();
-        if (!landed) stopped = true;
       }
       tmem_wait_st();
       tmem_fence_before_sync();
-      // a thread that gave up hands over nothing; its pair leaves at the next tile's meeting
-      if (!stopped) mbar_arrive(smem_addr(&p_full[g]));
+      // a warp that gave up hands over nothing; its pair leaves at the next tile's meeting
+      if (!__any_sync(0xffffffffu, stopped)) warp_arrive(smem_addr(&p_full[g]));
     }
-
-    // ---- join the four (group, half) sums of each row; every softmax thread meets here
     bool ok = !stopped;
-    if (ok) ok = mbar_wait(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
-    float* red = reinterpret_cast<float*>(smem);  // Q and the rings are done once drained
+    if (ok) ok = mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
     if (!ok) softmax_stop = 1;
-    asm volatile("bar.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
-    ok = !*reinterpret_cast<volatile int*>(&softmax_stop);
-    if (ok) {
+    softmax_sync();
+    if (!*reinterpret_cast<volatile int*>(&softmax_stop)) {
+      float* red = reinterpret_cast<float*>(smem);  // Q is done once drained
       red[(g * 2 + h) * C::kRows + r] = l_run;
       if (h == 0) red[(4 + g) * C::kRows + r] = m_run;
     }
-    asm volatile("bar.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
-    if (!ok) {
-      if (g == 0 && h == 0) no_result(r);
-    } else {
-      tmem_fence_after_sync();
-      const float m0 = red[4 * C::kRows + r], m1 = ntiles > 1 ? red[5 * C::kRows + r] : -INFINITY;
-      const float m = fmaxf(m0, m1), base = m == -INFINITY ? 0.f : m;
-      const float l = (red[r] + red[C::kRows + r]) * ex2_approx((m0 - base) * mul) +
-                      (red[2 * C::kRows + r] + red[3 * C::kRows + r]) * ex2_approx((m1 - base) * mul);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t cell =
-          (static_cast<int64_t>(row0 + tok) * a.num_q_heads + 2 * head + map) * nsplit + split;
-      if (rv && g == 0 && h == 0) {
-        a.chunk_m[cell] = m * mul;
-        a.chunk_l[cell] = l;
-      }
-      constexpr int kCols = 2 * D / 4;  // output columns of this thread
-      const int col0 = (g * 2 + h) * kCols;
+  }
+  __syncthreads();
+
+  // ---- the row's sum; then rows change sides: CTA `map` finishes rows 64 map .. 64 map + 63
+  const int ch = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;  // softmax warps
+  const bool mine = (quarter >> 1) == map, softmax = warp < kKWarp;
+  const bool rv = softmax && real_row(r);
+  const int head = pair * a.group + r % a.group;
+  const uint32_t obuf = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + C::kOCol;
+  const float* red = reinterpret_cast<const float*>(smem);
+  const bool ok = !softmax_stop;
+  constexpr int kCols = 2 * D / 4;  // this thread's columns: kCols ch ..
+  const float mul = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;
+  float inv = 0.f;
+  tmem_fence_after_sync();
+  if (softmax && ok) {
+    const float m0 = red[4 * C::kRows + r], m1 = ntiles > 1 ? red[5 * C::kRows + r] : -INFINITY;
+    const float m = fmaxf(m0, m1), base = m == -INFINITY ? 0.f : m;
+    const float l = (red[r] + red[C::kRows + r]) * ex2_approx((m0 - base) * mul) +
+                    (red[2 * C::kRows + r] + red[3 * C::kRows + r]) * ex2_approx((m1 - base) * mul);
+    inv = l > 0.f ? 1.f / l : 0.f;
+    if (nsplit > 1 && rv && ch == 0) {
+      a.chunk_m[cell(r)] = m * mul;
+      a.chunk_l[cell(r)] = l;
+    }
+  }
+  if (nsplit > 1) {
+    if (softmax && !ok && ch == 0) no_result(r);
+    if (softmax && ok) {
 #pragma unroll
-      for (int c0 = 0; c0 < kCols; c0 += 16) {
-        uint32_t t[16];
-        tmem_ld16(obuf + col0 + c0, t);
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
+        uint32_t t[32];
+        tmem_ld32(obuf + ch * kCols + c0, t);
         tmem_wait_ld();
         tmem_regs_ready(t);
         if (rv) {
 #pragma unroll
-          for (int c = 0; c < 16; c += 4)
-            *reinterpret_cast<float4*>(a.chunk_o + cell * (2 * D) + col0 + c0 + c) =
-                make_float4(__uint_as_float(t[c]) * inv, __uint_as_float(t[c + 1]) * inv,
-                            __uint_as_float(t[c + 2]) * inv, __uint_as_float(t[c + 3]) * inv);
+          for (int c = 0; c < 32; c += 4)
+            store4(a.chunk_o + cell(r) * (2 * D) + ch * kCols + c0 + c, t, c, inv);
         }
+      }
+    }
+  } else {
+    cluster_sync();  // both CTAs' rings are done with: V's takes the other map's 64 rows
+    // [row of the half][64 chunks of 16 bytes], chunk XORed with the row: conflict-free both ways
+    auto chunk_at = [&](uint32_t base, int row, int c) {
+      return base + row * (2 * D * 4) + ((c ^ (row & 7)) << 4);
+    };
+    if (softmax && !mine) {
+      const uint32_t there = cluster_addr(v_s, map ^ 1);
+      if (ok) {
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 32) {
+          uint32_t t[32];
+          tmem_ld32(obuf + ch * kCols + c0, t);
+          tmem_wait_ld();
+          tmem_regs_ready(t);
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             chunk_at(there, r & 63, (ch * kCols + c0 + c) / 4)),
+                         "f"(__uint_as_float(t[c]) * inv), "f"(__uint_as_float(t[c + 1]) * inv),
+                         "f"(__uint_as_float(t[c + 2]) * inv), "f"(__uint_as_float(t[c + 3]) * inv)
+                         : "memory");
+        }
+        if (lane == 0 && ch == 0 && (quarter & 1) == 0)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                           cluster_addr(smem_addr(&peer_stop), map ^ 1)),
+                       "r"(0)
+                       : "memory");
+      }
+    }
+    cluster_sync();
+    if (softmax && mine && ok && !*reinterpret_cast<volatile int*>(&peer_stop)) {
+      const int64_t row = tile.row0 + tile.qbase + (rv ? r / a.group : 0);
+      const float lam = __ldg(a.lam + row * a.lam_stride + head);
+      // 32 columns at a time, once for the row's sum of squares, once for the output (the
+      // registers do not hold 64 columns)
+      auto apart = [&](float own, float other) {
+        return map == 0 ? difference(own, other, lam) : difference(other, own, lam);
+      };
+      auto columns = [&](int c0, float (&y)[32]) {
+        uint32_t t[32];
+        tmem_ld32(obuf + c0, t);
+        tmem_wait_ld();
+        tmem_regs_ready(t);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          float4 p;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w)
+                       : "r"(chunk_at(v_s, r & 63, (c0 + c) / 4))
+                       : "memory");
+          y[c] = apart(__fmul_rn(__uint_as_float(t[c]), inv), p.x);
+          y[c + 1] = apart(__fmul_rn(__uint_as_float(t[c + 1]), inv), p.y);
+          y[c + 2] = apart(__fmul_rn(__uint_as_float(t[c + 2]), inv), p.z);
+          y[c + 3] = apart(__fmul_rn(__uint_as_float(t[c + 3]), inv), p.w);
+        }
+      };
+      float y[32], sum = 0.f;
+      if (a.norm_w) {
+        float ss = 0.f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kCols; c0 += 32) {
+          columns(ch * kCols + c0, y);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) ss += y[c] * y[c];
+        }
+        float* sq = reinterpret_cast<float*>(smem) + 6 * C::kRows;
+        sq[ch * C::kRows + r] = ss;
+        asm volatile("bar.sync 10, 256;" ::: "memory");  // the 8 warps of these rows
+        sum = (sq[r] + sq[C::kRows + r]) + (sq[2 * C::kRows + r] + sq[3 * C::kRows + r]);
+      }
+      __half* out = a.out + (row * (a.num_q_heads / 2) + head) * (2 * D);
+#pragma unroll 1
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
+        columns(ch * kCols + c0, y);
+        if (rv) finish_columns<D, BF, 32>(a, y, sum, out, ch * kCols + c0);
       }
     }
   }
@@ -494,17 +1001,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(C::kTmemCols)
-                 : "memory");
+  if (warp == 0) free_tmem(tmem, C::kTmemCols);
 }
 
-template <int D, int BS, bool BF>
-cudaError_t launch_t(const DiffArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                     cudaStream_t stream) {
-  using C = ChunkCfg<D>;
-  auto kern = diff_chunk_kernel<D, BS, BF>;
+template <typename C, typename K>
+cudaError_t launch_t(K kern, const DiffArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                     int ctas_per_tile, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -515,26 +1017,29 @@ cudaError_t launch_t(const DiffArgs& a, const CUtensorMap& kmap, const CUtensorM
       attr.numRegs * C::kThreads > 65536)
     return cudaErrorInvalidConfiguration;
   const int tile_q = C::kRows / a.group;
-  const dim3 grid(2 * ((a.max_query_len + tile_q - 1) / tile_q), a.num_pairs,
+  const dim3 grid(ctas_per_tile * ((a.max_query_len + tile_q - 1) / tile_q), a.num_pairs,
                   a.prefill_seqs * a.key_splits);
   kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(kmap, vmap, a);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int BS, bool BF>
 cudaError_t launch_d(const DiffArgs& a, const CUtensorMap& k, const CUtensorMap& v,
                      cudaStream_t st) {
-  if (a.block_size == 16)
-    return a.bf16 ? launch_t<D, 16, true>(a, k, v, st) : launch_t<D, 16, false>(a, k, v, st);
-  return a.bf16 ? launch_t<D, 32, true>(a, k, v, st) : launch_t<D, 32, false>(a, k, v, st);
+  return a.head_dim == 128
+             ? launch_t<MapCfg>(diff_chunk_map_kernel<BS, BF>, a, k, v, 2, st)
+             : launch_t<BothCfg>(diff_chunk_both_kernel<BS, BF>, a, k, v, 1, st);
 }
 
 }  // namespace
 
 cudaError_t launch_diff_chunk(const DiffArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                               cudaStream_t stream) {
-  return a.head_dim == 128 ? launch_d<128>(a, kmap, vmap, stream)
-                           : launch_d<64>(a, kmap, vmap, stream);
+  if (a.block_size == 16)
+    return a.bf16 ? launch_d<16, true>(a, kmap, vmap, stream)
+                  : launch_d<16, false>(a, kmap, vmap, stream);
+  return a.bf16 ? launch_d<32, true>(a, kmap, vmap, stream)
+                : launch_d<32, false>(a, kmap, vmap, stream);
 }
 
 }  // namespace pa
