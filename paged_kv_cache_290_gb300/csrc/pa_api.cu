@@ -208,6 +208,25 @@ int make_pool_map(CUtensorMap* m, void* base, int64_t rows, int d, int dtype) {
   return PA_OK;
 }
 
+int make_pair_map(CUtensorMap* m, void* base, int64_t tiles, int bs, int d, int dtype) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(bs), static_cast<cuuint64_t>(tiles),
+                        static_cast<cuuint64_t>(d / 64)};
+  cuuint64_t strides[3] = {row, row * bs, 128};
+  cuuint32_t box[4] = {64, 16, 2, static_cast<cuuint32_t>(d / 64)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(r));
+  return PA_OK;
+}
+
 const char* dtype_name(int dt) {
   switch (dt) {
     case PA_F16: return "float16";

@@ -189,18 +189,9 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
     const uint32_t dst = ring + st * C::kStageBytes;
     const int y = unit_row[warp + i * C::kWarps];
     mbar_arrive_expect_tx(bar, C::kStageBytes);
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h)
-        tma_load_2d_hint(dst + m * C::kHeadBytes + h * C::kBoxBytes, &kmap, h * 64, y + m * BS,
-                         bar, pol);
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h)
-        tma_load_2d_hint(dst + (2 + m) * C::kHeadBytes + h * C::kBoxBytes, &vmap, h * 64,
-                         y + m * BS, bar, pol);
+    // one box each: [half][head][16 rows][128 B]
+    tma_load_4d_hint(dst, &kmap, 0, y % BS, y / BS, 0, bar, pol);
+    tma_load_4d_hint(dst + 2 * C::kHeadBytes, &vmap, 0, y % BS, y / BS, 0, bar, pol);
   };
   grid_dependency_wait();  // q and the pools now hold what the kernels before wrote
   if (lane == 0) {
@@ -271,7 +262,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
         const int tok = mr + ((mi & 1) << 3);
         const int chunk = 2 * k + (mi >> 1);
         uint32_t af[4];
-        ldsm_x4(kb + m * C::kHeadBytes + (chunk >> 3) * C::kBoxBytes + swz128(tok, chunk & 7), af);
+        ldsm_x4(kb + (chunk >> 3) * (2 * C::kBoxBytes) + m * C::kBoxBytes + swz128(tok, chunk & 7), af);
         mma_16816<BF>(sacc[m], af, qf[nt][k][0], qf[nt][k][1]);
       }
     }
@@ -346,9 +337,10 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
 #pragma unroll
     for (int dt = 0; dt < C::kMT; ++dt) {
       const int tok = mr + ((mi >> 1) << 3);
-      const int chunk = 2 * dt + (mi & 1);  // of the 2d-wide row
+      const int chunk = 2 * dt + (mi & 1);  // of the 2d-wide row: head, half, 16-byte chunk
+      const int half = (chunk >> 3) % C::kHalves, hd = (chunk >> 3) / C::kHalves;
       uint32_t af[4];
-      ldsm_x4_trans(vb + (chunk >> 3) * C::kBoxBytes + swz128(tok, chunk & 7), af);
+      ldsm_x4_trans(vb + half * (2 * C::kBoxBytes) + hd * C::kBoxBytes + swz128(tok, chunk & 7), af);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma_16816<BF>(o[nt][dt], af, pb0[nt], pb1[nt]);
     }
@@ -824,12 +816,16 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   cudaError_t e = error_word(stream, &a.err);
   if (e != cudaSuccess) return cuda_fail(e, "error word");
   const int64_t rows = k_cache->shape[0] * hkv * k_cache->shape[2];
-  CUtensorMap kmap, vmap;
-  if ((rc = make_pool_map(&kmap, k_cache->data, rows, static_cast<int>(d), dt))) return rc;
-  if ((rc = make_pool_map(&vmap, v_cache->data, rows, static_cast<int>(d), dt))) return rc;
+  const int64_t tiles = k_cache->shape[0] * hkv;
+  // kmap: one head's 16 rows a box; kpair, vpair: both heads of a pair
+  CUtensorMap kmap{}, kpair{}, vpair{};
+  const int bs = a.block_size, di = a.head_dim;
+  if (plan.chunks && (rc = make_pool_map(&kmap, k_cache->data, rows, di, dt))) return rc;
+  if (plan.rows && (rc = make_pair_map(&kpair, k_cache->data, tiles, bs, di, dt))) return rc;
+  if ((rc = make_pair_map(&vpair, v_cache->data, tiles, bs, di, dt))) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto chunks = [&](cudaStream_t on) -> int {
-    cudaError_t ce = launch_diff_chunk(a, kmap, vmap, on);
+    cudaError_t ce = launch_diff_chunk(a, kmap, vpair, on);
     if (ce != cudaSuccess) return cuda_fail(ce, "diff chunk launch");
     if (a.key_splits > 1) ce = launch_diff_chunk_merge(a, on);
     return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "diff chunk merge launch");
@@ -858,7 +854,7 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
     join.st = st;
     if ((rc = chunks(side->stream))) return rc;
   }
-  if ((e = launch_diff_rows(a, kmap, vmap, st)) != cudaSuccess) return cuda_fail(e, "diff launch");
+  if ((e = launch_diff_rows(a, kpair, vpair, st)) != cudaSuccess) return cuda_fail(e, "diff launch");
   if (a.max_parts > 1 && (e = launch_diff_merge(a, st)) != cudaSuccess)
     return cuda_fail(e, "diff merge launch");
   if ((e = join.done()) != cudaSuccess) return cuda_fail(e, "stream join");

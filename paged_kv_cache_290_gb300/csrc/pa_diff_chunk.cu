@@ -56,9 +56,8 @@ struct BothCfg : ChunkCfg {                       // d = 64
 
 struct MapCfg : ChunkCfg {                        // d = 128
   static constexpr int kTileBytes = 2 * 128 * 128;  // 128 rows of one head
-  static constexpr int kVKeys = 64;               // keys of a V piece
-  static constexpr int kVBytes = 4 * kVKeys * 128;  // both heads
-  static constexpr int kKStages = 2, kVStages = 4;
+  static constexpr int kVBytes = 2 * kTileBytes;    // both heads
+  static constexpr int kKStages = 2, kVStages = 2;
   static constexpr int kSmemBytes = kTileBytes + kKStages * kTileBytes + kVStages * kVBytes + 1024;
   static_assert(kSmemBytes + 2048 <= 232448, "dynamic + static shared memory fit one SM");
   static_assert(kVStages * kVBytes >= 64 * 2 * 128 * 4, "64 rows of the other map fit V's ring");
@@ -142,15 +141,17 @@ __device__ __forceinline__ bool bad_blocks(const DiffArgs& a, const Tile& t) {
   return bad;
 }
 
-// A producer warp: streams kPart-key pieces of `heads` heads from head0 on into a ring; lane u
-// fetches unit u (16 keys), whose block id it reads a piece ahead.  Before returning it waits
-// for its last copies, so none lands after the CTA retires.
-template <int D, int BS, int kPart>
+// A producer warp: streams 128-key tiles of `heads` heads from head0 on into a ring; lane u
+// fetches unit u (16 keys), whose block id it reads a tile ahead.  K (kPairs false): one box per
+// head and 64 columns, into [head][half][128 keys][128 B].  V (kPairs true): one box of both
+// heads, into [unit][half][head][16 keys][128 B].  Before returning it waits for its last
+// copies, so none lands after the CTA retires.
+template <int D, int BS, bool kPairs>
 __device__ __forceinline__ void stream_heads(const DiffArgs& a, const Tile& t,
                                              const CUtensorMap* tm, int head0, int heads,
                                              int stages, uint64_t* full, uint64_t* empty,
                                              uint32_t ring) {
-  constexpr int kHalves = D / 64, kUnits = kPart / 16;
+  constexpr int kHalves = D / 64, kPart = 128, kUnits = kPart / 16;
   const int lane = threadIdx.x & 31;
   const int pieces = (t.key_stop - t.key_base + kPart - 1) / kPart;
   const int stage_bytes = heads * kHalves * kPart * 128;
@@ -175,12 +176,19 @@ __device__ __forceinline__ void stream_heads(const DiffArgs& a, const Tile& t,
     if (lane == 0) mbar_arrive_expect_tx(bar, units * heads * kHalves * 2048);
     __syncwarp();
     if (lane < units) {
-      const int y = (blk * a.num_kv_heads + head0) * BS + (t.key_base + j * kPart + 16 * lane) % BS;
-      const uint32_t dst = ring + st * stage_bytes + lane * 2048;
-      for (int h = 0; h < heads; ++h)
+      const int off = (t.key_base + j * kPart + 16 * lane) % BS;
+      const uint32_t dst = ring + st * stage_bytes;
+      if constexpr (kPairs) {
+        tma_load_4d(dst + lane * (2 * kHalves * 2048), tm, 0, off, blk * a.num_kv_heads + head0, 0,
+                    bar);
+      } else {
+        const int y = (blk * a.num_kv_heads + head0) * BS + off;
+        for (int h = 0; h < heads; ++h)
 #pragma unroll
-        for (int c = 0; c < kHalves; ++c)
-          tma_load_2d(dst + (h * kHalves + c) * (kPart * 128), tm, c * 64, y + h * BS, bar);
+          for (int c = 0; c < kHalves; ++c)
+            tma_load_2d(dst + (h * kHalves + c) * (kPart * 128) + lane * 2048, tm, c * 64,
+                        y + h * BS, bar);
+      }
     }
     issued = j + 1;
   }
@@ -257,14 +265,14 @@ __device__ __forceinline__ void rescale(uint32_t addr, int n, float f) {
   }
 }
 
-// n chunks of 16 bytes at `row` of a 128-byte-swizzled tile's rows are cleared (a whole row of
-// each 64-column half, so the swizzle does not matter).
-template <int kHalves, int kPart>
-__device__ __forceinline__ void clear_row(uint32_t row) {
+// Clears row r of head h of a V tile (whole 128-byte rows, so the swizzle does not matter).
+template <int kHalves>
+__device__ __forceinline__ void clear_v_row(uint32_t tile, int r, int h) {
+  const uint32_t row = tile + (r >> 4) * (2 * kHalves * 2048) + h * 2048 + (r & 15) * 128;
 #pragma unroll
   for (int c = 0; c < kHalves * 8; ++c)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                     row + (c >> 3) * (kPart * 128) + (c & 7) * 16),
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + (c >> 3) * 4096 +
+                                                                  (c & 7) * 16),
                  "r"(0u)
                  : "memory");
 }
@@ -412,55 +420,70 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     // ================================================ producer / MMA warpgroup
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kKWarp) {
-      stream_heads<D, BS, C::kKeys>(a, tile, &kmap, 2 * pair, 2, C::kKStages, k_full, k_empty, k_s);
+      stream_heads<D, BS, false>(a, tile, &kmap, 2 * pair, 2, C::kKStages, k_full, k_empty, k_s);
     } else if (warp == kVWarp) {
-      stream_heads<D, BS, C::kKeys>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s);
+      stream_heads<D, BS, true>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s);
     } else if (warp == kMmaWarp && lane == 0) {
       constexpr uint32_t kIdS = umma_idesc_f16(C::kRows, C::kKeys, 0, 0, BF);
       constexpr uint32_t kIdO = umma_idesc_f16(C::kRows, 2 * D, 0, 1, BF);
-      auto issue_s = [&](int t, int j) {
-        const uint32_t qb = q_s + t * C::kTileBytes;
-        const uint32_t kb = k_s + (j % C::kKStages) * C::kStageBytes + t * C::kTileBytes;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          umma_f16(tmem + t * 128, umma_sdesc(qb + k * 32, 16, 1024),
-                   umma_sdesc(kb + k * 32, 16, 1024), kIdS, k > 0);
-        umma_commit(smem_addr(&s_full[t]));
-      };
-      auto kwait = [&](int j) {
-        const bool ok = mbar_wait_short(smem_addr(&k_full[j % C::kKStages]),
-                                        (j / C::kKStages) & 1, a.err, a.wait_limit_ns);
+      // The pipe queues almost nothing, so a wait between two products idles it for the wait's own
+      // latency even when the barrier is long complete.  So each barrier is tested while products
+      // issued before are still running, and waited for only when that test failed.
+      auto k_bar = [&](int j) { return smem_addr(&k_full[j % C::kKStages]); };
+      auto v_bar = [&](int j) { return smem_addr(&v_full[j % C::kVStages]); };
+      auto need = [&](bool seen, uint32_t bar, int phase) {
+        const bool ok = seen || mbar_wait_short(bar, phase & 1, a.err, a.wait_limit_ns);
         tmem_fence_after_sync();
         return ok;
       };
-      bool ok = mbar_wait_short(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) && kwait(0);
+      // S_t(j); tests P of the product to follow halfway
+      bool p_seen = false, v_seen = false, k_seen = false;
+      auto issue_s = [&](int t, int j, uint32_t next_p, int next_phase) {
+        const uint32_t qb = q_s + t * C::kTileBytes;
+        const uint32_t kb = k_s + (j % C::kKStages) * C::kStageBytes + t * C::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          if (k == D / 16 - 1 && next_phase >= 0) p_seen = mbar_test(next_p, next_phase & 1);
+          umma_f16(tmem + t * 128, umma_sdesc(qb + k * 32, 16, 1024),
+                   umma_sdesc(kb + k * 32, 16, 1024), kIdS, k > 0);
+        }
+        umma_commit(smem_addr(&s_full[t]));
+      };
+      bool ok = mbar_wait_short(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) &&
+                need(false, k_bar(0), 0);
       if (ok) {
-        issue_s(0, 0);
-        issue_s(1, 0);
+        issue_s(0, 0, 0, -1);
+        issue_s(1, 0, 0, -1);
         umma_commit(smem_addr(&k_empty[0]));
       }
       for (int j = 0; ok && j < ntiles; ++j) {
         const int vst = j % C::kVStages;
         const uint32_t vb = v_s + vst * C::kStageBytes;
-        ok = mbar_wait_short(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err,
-                             a.wait_limit_ns);
+        const bool more = j + 1 < ntiles;
+        ok = need(v_seen, v_bar(j), j / C::kVStages);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          ok = ok && mbar_wait_short(smem_addr(&p_full[t]), j & 1, a.err, a.wait_limit_ns);
+          ok = ok && need(p_seen, smem_addr(&p_full[t]), j);
           if (!ok) break;
-          tmem_fence_after_sync();
+          p_seen = false;
 #pragma unroll
-          for (int k = 0; k < C::kKeys / 16; ++k)
+          for (int k = 0; k < C::kKeys / 16; ++k) {
+            if (k == 6 && more) {
+              if (t == 0)
+                k_seen = mbar_test(k_bar(j + 1), (j + 1) / C::kKStages & 1);
+              else
+                v_seen = mbar_test(v_bar(j + 1), (j + 1) / C::kVStages & 1);
+            }
             umma_f16_tmem_a(tmem + C::kOCol + t * 128, tmem + t * 128 + k * 8,
-                            umma_sdesc(vb + k * 16 * 128, C::kKeys * 128, 1024), kIdO,
-                            (j > 0 || k > 0));
+                            umma_sdesc(vb + k * 4096, 2048, 1024), kIdO, (j > 0 || k > 0));
+          }
           if (t == 1) umma_commit(smem_addr(&v_empty[vst]));
-          if (j + 1 < ntiles) {
-            if (t == 0) ok = kwait(j + 1);
-            if (ok) issue_s(t, j + 1);
+          if (more) {
+            if (t == 0) ok = need(k_seen, k_bar(j + 1), (j + 1) / C::kKStages);
+            if (ok) issue_s(t, j + 1, smem_addr(&p_full[t ^ 1]), t == 0 ? j : j + 1);
           }
         }
-        if (ok && j + 1 < ntiles) umma_commit(smem_addr(&k_empty[(j + 1) % C::kKStages]));
+        if (ok && more) umma_commit(smem_addr(&k_empty[(j + 1) % C::kKStages]));
       }
       umma_commit(smem_addr(&drain));
       mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
@@ -539,7 +562,7 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
                              a.wait_limit_ns))
           stopped = true;
         else if (tile0 + r >= tile.key_stop)
-          clear_row<1, C::kKeys>(v_s + vst * C::kStageBytes + h * C::kTileBytes + r * 128);
+          clear_v_row<1>(v_s + vst * C::kStageBytes, r, h);
         fence_proxy_async();
       }
       tmem_wait_st();
@@ -692,61 +715,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_base;
   const int ntiles = tile.ntiles;
-  const int pieces = (tile.key_stop - tile.key_base + C::kVKeys - 1) / C::kVKeys;
 
   constexpr int kKWarp = C::kSoftmax / 32, kVWarp = kKWarp + 1, kMmaWarp = kKWarp + 2;
   if (warp >= kKWarp) {
     // ================================================ producer / MMA warpgroup
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kKWarp) {
-      stream_heads<D, BS, C::kKeys>(a, tile, &kmap, 2 * pair + map, 1, C::kKStages, k_full,
-                                    k_empty, k_s);
+      stream_heads<D, BS, false>(a, tile, &kmap, 2 * pair + map, 1, C::kKStages, k_full, k_empty,
+                                 k_s);
     } else if (warp == kVWarp) {
-      // V in pieces of 64 keys: a piece's stage is refilled as soon as its half of P V is done
-      stream_heads<D, BS, C::kVKeys>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty,
-                                     v_s);
+      stream_heads<D, BS, true>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s);
     } else if (warp == kMmaWarp && lane == 0) {
       constexpr uint32_t kIdS = umma_idesc_f16(C::kRows, C::kKeys, 0, 0, BF);
       constexpr uint32_t kIdO = umma_idesc_f16(C::kRows, 2 * D, 0, 1, BF);
-      auto issue_s = [&](int j) {
-        const int st = j % C::kKStages;
-        if (!mbar_wait_short(smem_addr(&k_full[st]), (j / C::kKStages) & 1, a.err,
-                             a.wait_limit_ns))
-          return false;
+      // As in the other kernel: barriers are tested while products still run.
+      auto k_bar = [&](int j) { return smem_addr(&k_full[j % C::kKStages]); };
+      auto v_bar = [&](int j) { return smem_addr(&v_full[j % C::kVStages]); };
+      auto need = [&](bool seen, uint32_t bar, int phase) {
+        const bool ok = seen || mbar_wait_short(bar, phase & 1, a.err, a.wait_limit_ns);
         tmem_fence_after_sync();
+        return ok;
+      };
+      bool p_seen = false, v_seen = false, k_seen = false;
+      auto issue_s = [&](int j, bool test) {  // test: V and P of tile j - 1, the products to follow
+        const int st = j % C::kKStages;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
+          if (k == 4 && test) v_seen = mbar_test(v_bar(j - 1), (j - 1) / C::kVStages & 1);
+          if (k == 6 && test) p_seen = mbar_test(smem_addr(&p_full[(j - 1) & 1]), (j - 1) >> 1 & 1);
           const uint32_t off = (k >> 2) * (C::kKeys * 128) + (k & 3) * 32;
           umma_f16(tmem + (j & 1) * 128, umma_sdesc(q_s + off, 16, 1024),
                    umma_sdesc(k_s + st * C::kTileBytes + off, 16, 1024), kIdS, k > 0);
         }
         umma_commit(smem_addr(&s_full[j & 1]));
         umma_commit(smem_addr(&k_empty[st]));
-        return true;
       };
-      bool ok = mbar_wait_short(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) && issue_s(0) &&
-                (ntiles < 2 || issue_s(1));
+      bool ok = mbar_wait_short(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) &&
+                need(false, k_bar(0), 0);
+      if (ok) issue_s(0, false);
+      if (ok && ntiles > 1) {
+        ok = need(false, k_bar(1), 1 / C::kKStages);
+        if (ok) issue_s(1, false);
+      }
       for (int j = 0; ok && j < ntiles; ++j) {
-        ok = mbar_wait_short(smem_addr(&p_full[j & 1]), (j >> 1) & 1, a.err, a.wait_limit_ns);
-        // a last tile of at most 64 keys has one piece: the other half of P is 0
-        for (int p = 2 * j; ok && p < min(2 * j + 2, pieces); ++p) {
-          const int vst = p % C::kVStages;
-          ok = mbar_wait_short(smem_addr(&v_full[vst]), (p / C::kVStages) & 1, a.err,
-                               a.wait_limit_ns);
-          if (!ok) break;
-          tmem_fence_after_sync();
-          const uint32_t vb = v_s + vst * C::kVBytes;
-#pragma unroll
-          for (int k = 0; k < C::kVKeys / 16; ++k)
-            umma_f16_tmem_a(tmem + C::kOCol,
-                            tmem + (j & 1) * 128 + ((p & 1) * (C::kVKeys / 16) + k) * 8,
-                            umma_sdesc(vb + k * 16 * 128, C::kVKeys * 128, 1024), kIdO,
-                            (p > 0 || k > 0));
-          umma_commit(smem_addr(&v_empty[vst]));
-        }
+        const int vst = j % C::kVStages;
+        const bool more = j + 2 < ntiles;
+        ok = need(v_seen, v_bar(j), j / C::kVStages) &&
+             need(p_seen, smem_addr(&p_full[j & 1]), j >> 1);
         if (!ok) break;
-        umma_commit(smem_addr(&pv_done));
-        if (j + 2 < ntiles) ok = issue_s(j + 2);
+        v_seen = p_seen = false;
+        const uint32_t vb = v_s + vst * C::kVBytes;
+#pragma unroll
+        for (int k = 0; k < C::kKeys / 16; ++k) {
+          if (k == 6 && more) k_seen = mbar_test(k_bar(j + 2), (j + 2) / C::kKStages & 1);
+          umma_f16_tmem_a(tmem + C::kOCol, tmem + (j & 1) * 128 + k * 8,
+                          umma_sdesc(vb + k * 8192, 2048, 1024), kIdO, (j > 0 || k > 0));
+        }
+        umma_commit(smem_addr(&v_empty[vst]));
+        if (more) {
+          ok = need(k_seen, k_bar(j + 2), (j + 2) / C::kKStages);
+          if (ok) issue_s(j + 2, true);
+        } else {
+          umma_commit(smem_addr(&pv_done));
+        }
       }
       umma_commit(smem_addr(&drain));
       mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
@@ -837,9 +868,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
         m_new = mx;
       }
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // rare: O so far, its last product done, goes over to the new base
-        if (!__all_sync(0xffffffffu, mbar_wait_short(smem_addr(&pv_done), (j - 1) & 1, a.err,
-                                                     a.wait_limit_ns)))
+        // rare: O so far, its last product done, goes over to the new base.  P V of tile j - 1 is
+        // done when S(j + 1), issued after it, is; the last tile has its own barrier.
+        const bool more = j + 1 < ntiles;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_short(smem_addr(more ? &s_full[(j + 1) & 1] : &pv_done),
+                                        more ? (j + 1) >> 1 & 1 : 0, a.err, a.wait_limit_ns)))
           stopped = true;
         tmem_fence_after_sync();
         rescale(obuf + h * D, D, alpha);
@@ -849,17 +883,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
       m_run = m_new;
       l_run += store_weights<BF>(sbuf + h * 32, sv, mul, m_run == -INFINITY ? 0.f : -m_run * mul);
 
-      const int last = pieces - 1, piece0 = tile.key_base + last * C::kVKeys;
-      if (j == ntiles - 1 && piece0 + C::kVKeys > tile.key_stop) {
-        // V rows past the last visible key may hold any bits: each thread clears half a row of
-        // head h in the last piece once that has landed
-        const int vst = last % C::kVStages, rr = r & (C::kVKeys - 1);
-        if (!mbar_wait_short(smem_addr(&v_full[vst]), (last / C::kVStages) & 1, a.err,
+      const int tile0 = tile.key_base + j * C::kKeys;
+      if (j == ntiles - 1 && tile0 + C::kKeys > tile.key_stop) {
+        // V rows past the last visible key may hold any bits: each thread clears row r of head h
+        // once the tile has landed
+        const int vst = j % C::kVStages;
+        if (!mbar_wait_short(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err,
                              a.wait_limit_ns))
           stopped = true;
-        else if (piece0 + rr >= tile.key_stop)
-          clear_row<1, C::kVKeys>(v_s + vst * C::kVBytes + (h * 2 + (r >> 6)) * (C::kVKeys * 128) +
-                                  rr * 128);
+        else if (tile0 + r >= tile.key_stop)
+          clear_v_row<2>(v_s + vst * C::kVBytes, r, h);
         fence_proxy_async();
       }
       tmem_wait_st();
@@ -887,7 +920,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   const uint32_t obuf = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + C::kOCol;
   const float* red = reinterpret_cast<const float*>(smem);
   const bool ok = !softmax_stop;
-  constexpr int kCols = 2 * D / 4;  // this thread's columns: kCols ch ..
+  constexpr int kCols = 2 * D / 4;  // this thread's columns: kCols ch .. of O
+  // O's 64-column pieces are in V's order (half, head); of y: (head, half)
+  const int out0 = ((ch & 1) * 2 + (ch >> 1)) * 64;
   const float mul = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;
   float inv = 0.f;
   tmem_fence_after_sync();
@@ -914,7 +949,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
         if (rv) {
 #pragma unroll
           for (int c = 0; c < 32; c += 4)
-            store4(a.chunk_o + cell(r) * (2 * D) + ch * kCols + c0 + c, t, c, inv);
+            store4(a.chunk_o + cell(r) * (2 * D) + out0 + c0 + c, t, c, inv);
         }
       }
     }
@@ -993,7 +1028,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
 #pragma unroll 1
       for (int c0 = 0; c0 < kCols; c0 += 32) {
         columns(ch * kCols + c0, y);
-        if (rv) finish_columns<D, BF, 32>(a, y, sum, out, ch * kCols + c0);
+        if (rv) finish_columns<D, BF, 32>(a, y, sum, out, out0 + c0);
       }
     }
   }

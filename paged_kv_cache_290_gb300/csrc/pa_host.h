@@ -31,6 +31,11 @@ int check_scales(const pa_kv_scales* sc);
 // The pool as a 2-D tensor map (16-row boxes; see pa_api.cu).
 int make_pool_map(CUtensorMap* m, void* base, int64_t rows, int d, int dtype);
 
+// A 16-bit pool [NB, Hkv, bs, d] as a 4-D tensor (64 values, bs rows, NB * Hkv tiles, d / 64
+// column halves) with boxes of 64 values x 16 rows x 2 adjacent heads x all halves, 128-byte
+// swizzle: one copy fetches 16 tokens of a pair of heads as [half][head][16 rows][128 B].
+int make_pair_map(CUtensorMap* m, void* base, int64_t tiles, int bs, int d, int dtype);
+
 cudaError_t device_sm_count(int* out);
 
 // A side stream and two events per device and host thread, for work beside the caller's stream.
