@@ -57,14 +57,6 @@ struct RowsCfg {
   static_assert(kStages >= 2, "stage ring");
 };
 
-template <bool BF>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if constexpr (BF)
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  else
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
 // y of one differential head (kV consecutive dims per lane, a warp per head) -> out.
 template <int D, bool BF>
 __device__ __forceinline__ void finish_head(const DiffArgs& a, float (&y)[2 * D / 32], int64_t row,
@@ -312,14 +304,12 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
       const float b1 = m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1];
       const float p00 = exp2f(sc[nt][0] - b0), p10 = exp2f(sc[nt][2] - b0);
       const float p01 = exp2f(sc[nt][1] - b1), p11 = exp2f(sc[nt][3] - b1);
+      l_run[nt][0] += p00 + p10;
+      l_run[nt][1] += p01 + p11;
       // P is rounded to the element type for the matrix product: at most 2^-11 (fp16) or 2^-8
-      // (bf16) of each weight.  l sums the rounded weights, so their errors cancel in part.
-      const uint32_t w0 = pack2<BF>(p00, p01), w1 = pack2<BF>(p10, p11);
-      const float2 f0 = unpack2<BF>(w0), f1 = unpack2<BF>(w1);
-      l_run[nt][0] += f0.x + f1.x;
-      l_run[nt][1] += f0.y + f1.y;
-      pb0[nt] = movmatrix_trans(w0);
-      pb1[nt] = movmatrix_trans(w1);
+      // (bf16) of each weight, at random over the keys
+      pb0[nt] = movmatrix_trans(pack2<BF>(p00, p01));
+      pb1[nt] = movmatrix_trans(pack2<BF>(p10, p11));
     }
 
     if (nvalid < 16) {  // V rows past the end: p is 0 there, but 0 * NaN is not
