@@ -8,8 +8,8 @@
 //     accumulators.  V is loaded once for both, and the CTA finishes its rows alone.
 //   * d = 128 (diff_chunk_map_kernel): one map's accumulator takes 256 columns and its two score
 //     buffers the rest, so a CTA holds one map and a cluster of two CTAs a Q tile; at the end
-//     each CTA sends the other half of its rows' sums through distributed shared memory and
-//     finishes 64 rows.  (Both maps in one CTA with half of V's width each would fit too, but
+//     each CTA copies half of its rows' sums into the other's shared memory and finishes the
+//     other 64 rows.  (Both maps in one CTA with half of V's width each would fit too, but
 //     every score and exponential would be computed twice: 8 tile products instead of 6.)
 //
 // 640 threads in both:
@@ -26,7 +26,6 @@
 
 #include <algorithm>
 
-#include "pa_chunk.cuh"
 #include "pa_common.cuh"
 #include "pa_diff.h"
 
@@ -84,24 +83,60 @@ struct Tile {
 };
 
 // Finds and checks the tile; false when the CTA has none (errors are reported).  All threads of
-// the block call it.
-template <int BS, int kThreads>
-__device__ __forceinline__ bool find_tile(const DiffArgs& a, int* warp_count, int* chosen_seq,
-                                          int qt, int z, int split, bool first, bool lead,
-                                          Tile& t) {
-  t.s = find_prefill_seq<kThreads>(a, warp_count, chosen_seq, z, first);
+// the block call it.  Grid row z serves the z-th sequence with more than one query row, in batch
+// order: a ballot scan in which every thread also holds its sequence's descriptor, so the chosen
+// one is handed on through shared memory without a second round of loads.
+struct TileScan {
+  int warp_count[ChunkCfg::kThreads / 32];
+  int s, row0, q_len, L;
+};
+template <int BS>
+__device__ __forceinline__ bool find_tile(const DiffArgs& a, TileScan& sc, int qt, int z, int split,
+                                          bool first, bool lead, Tile& t) {
+  constexpr int kThreads = ChunkCfg::kThreads;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) sc.s = -1;
+  int found = 0;
+  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
+    const int si = s0 + tid;
+    const bool in = si < a.num_seqs;
+    const int row0 = in ? a.query_start_loc[si] : 0;
+    const int q_len = in ? a.query_start_loc[si + 1] - row0 : 0;
+    const int L = in ? a.seq_lens[si] : 0;
+    const unsigned bal = __ballot_sync(0xffffffffu, q_len > 1);
+    if (a.decode_skipped && first && __any_sync(0xffffffffu, q_len == 1) && lane == 0)
+      atomicOr(a.err, kErrHint);
+    if (lane == 0) sc.warp_count[warp] = __popc(bal);
+    __syncthreads();
+    int rank = found + __popc(bal & ((1u << lane) - 1u));
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      rank += w < warp ? sc.warp_count[w] : 0;
+      found += sc.warp_count[w];
+    }
+    if (q_len > 1 && rank == z) {
+      sc.s = si;
+      sc.row0 = row0;
+      sc.q_len = q_len;
+      sc.L = L;
+    }
+    __syncthreads();
+  }
+  __syncthreads();
+  if (first && tid == 0 && found > a.prefill_seqs) atomicOr(a.err, kErrHint);
+  t.s = sc.s;
   if (t.s < 0) return false;
   t.tile_q = 128 / a.group;
-  t.row0 = a.query_start_loc[t.s];
-  t.q_len = a.query_start_loc[t.s + 1] - t.row0;
-  const int L = a.seq_lens[t.s];
+  t.row0 = sc.row0;
+  t.q_len = sc.q_len;
+  const int L = sc.L;
   if (t.q_len > L || (L + BS - 1) / BS > a.max_blocks || t.row0 < 0 ||
       t.row0 + t.q_len > a.num_tokens) {
-    if (lead && threadIdx.x == 0) atomicOr(a.err, kErrDescriptor);
+    if (lead && tid == 0) atomicOr(a.err, kErrDescriptor);
     return false;
   }
   if (t.q_len > a.max_query_len || L > a.max_seq_len) {
-    if (lead && threadIdx.x == 0) atomicOr(a.err, kErrHint);
+    if (lead && tid == 0) atomicOr(a.err, kErrHint);
     return false;
   }
   t.qbase = qt * t.tile_q;
@@ -117,28 +152,17 @@ __device__ __forceinline__ bool find_tile(const DiffArgs& a, int* warp_count, in
   return true;
 }
 
-// Whether a block id of the tile's keys is outside the pool (this thread's share).
-template <int BS, int kThreads>
-__device__ __forceinline__ bool bad_blocks(const DiffArgs& a, const Tile& t) {
-  bool bad = false;
-  for (int i = t.key_base / BS + static_cast<int>(threadIdx.x); i < (t.key_stop + BS - 1) / BS;
-       i += kThreads) {
-    const int32_t blk = a.block_tables[static_cast<int64_t>(t.s) * a.bt_stride + i];
-    bad |= blk < 0 || blk >= a.num_blocks;
-  }
-  return bad;
-}
-
 // A producer warp: streams 128-key tiles of `heads` heads from head0 on into a ring; lane u
 // fetches unit u (16 keys), whose block id it reads a tile ahead.  K (kPairs false): one box per
 // head and 64 columns, into [head][half][128 keys][128 B].  V (kPairs true): one box of both
 // heads, into [unit][half][head][16 keys][128 B].  Before returning it waits for its last
-// copies, so none lands after the CTA retires.
+// copies, so none lands after the CTA retires.  A block id outside the pool is reported, sets
+// *stop (no row of the tile is written then) and block 0 is fetched in its place.
 template <int D, int BS, bool kPairs>
 __device__ __forceinline__ void stream_heads(const DiffArgs& a, const Tile& t,
                                              const CUtensorMap* tm, int head0, int heads,
                                              int stages, uint64_t* full, uint64_t* empty,
-                                             uint32_t ring) {
+                                             uint32_t ring, int* stop) {
   constexpr int kHalves = D / 64, kPart = 128, kUnits = kPart / 16;
   const int lane = threadIdx.x & 31;
   const int pieces = (t.key_stop - t.key_base + kPart - 1) / kPart;
@@ -153,7 +177,13 @@ __device__ __forceinline__ void stream_heads(const DiffArgs& a, const Tile& t,
   };
   int issued = 0, next = block_of(0);
   for (int j = 0; j < pieces; ++j) {
-    const int st = j % stages, round = j / stages, blk = next;
+    const int st = j % stages, round = j / stages;
+    int blk = next;
+    if (blk < 0 || blk >= a.num_blocks) {
+      atomicOr(a.err, kErrBlockRange);
+      *reinterpret_cast<volatile int*>(stop) = 1;
+      blk = 0;
+    }
     if (j + 1 < pieces) next = block_of(j + 1);
     bool ok = true;
     if (lane == 0 && round > 0)
@@ -319,12 +349,19 @@ __device__ __forceinline__ void finish_columns(const DiffArgs& a, float (&y)[kCo
 // All 512 softmax threads meet.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 9, 512;" ::: "memory"); }
 
-// All threads of both CTAs of the cluster meet; their shared-memory accesses before are visible
-// after.
-__device__ __forceinline__ void cluster_sync() {
+// All threads of both CTAs of the cluster meet; their shared-memory accesses before the arrival
+// are visible after the wait.
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 
 // The address of `addr` (of this CTA's shared memory) in the CTA of cluster rank `rank`.
@@ -345,8 +382,8 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   __shared__ __align__(8) uint64_t v_full[C::kVStages], v_empty[C::kVStages];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, drain;
   __shared__ uint32_t tmem_base;
-  __shared__ int warp_count[C::kThreads / 32];
-  __shared__ int chosen_seq, softmax_stop;
+  __shared__ TileScan scan;
+  __shared__ int softmax_stop;
   __shared__ float half_max[2][2][C::kRows];  // [map][half][row], of the latest tile
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -359,9 +396,9 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   const int pair = blockIdx.y, nsplit = a.key_splits;
   const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
   Tile tile;
-  if (!find_tile<BS, C::kThreads>(a, warp_count, &chosen_seq, gridDim.x - 1 - blockIdx.x, z, split,
-                                  blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
-                                  blockIdx.x == 0 && split == 0, tile))
+  if (!find_tile<BS>(a, scan, gridDim.x - 1 - blockIdx.x, z, split,
+                     blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
+                     blockIdx.x == 0 && split == 0, tile))
     return;
   // the cell of a row's partial, when the keys are split
   auto cell = [&](int row, int map) {
@@ -375,12 +412,18 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   auto no_result = [&](int row, int map) {
     if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row, map)] = -1.f;
   };
-  if (__syncthreads_or(bad_blocks<BS, C::kThreads>(a, tile))) {
-    if (tid == 0) atomicOr(a.err, kErrBlockRange);
-    if (tid < 2 * C::kRows) no_result(tid >> 1, tid & 1);
-    return;
+  // This thread's share of Q (half a row of its map), in flight while the barriers are set up.
+  uint4 qv[D / 16];
+  if (warp < C::kSoftmax / 32) {
+    const int r = (warp & 3) * 32 + lane, h = (warp >> 2) & 1, g = warp >> 3;
+    const bool rv = real_row(r);
+    const __half* qrow =
+        a.q + static_cast<int64_t>(tile.row0 + tile.qbase + (rv ? r / a.group : 0)) * a.q_stride +
+        static_cast<int64_t>(2 * (pair * a.group + r % a.group) + g) * D + h * (D / 2);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+      qv[c] = rv ? __ldg(reinterpret_cast<const uint4*>(qrow) + c) : make_uint4(0u, 0u, 0u, 0u);
   }
-
   if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < C::kKStages; ++i) {
@@ -411,9 +454,11 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     // ================================================ producer / MMA warpgroup
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kKWarp) {
-      stream_heads<D, BS, false>(a, tile, &kmap, 2 * pair, 2, C::kKStages, k_full, k_empty, k_s);
+      stream_heads<D, BS, false>(a, tile, &kmap, 2 * pair, 2, C::kKStages, k_full, k_empty, k_s,
+                                 &softmax_stop);
     } else if (warp == kVWarp) {
-      stream_heads<D, BS, true>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s);
+      stream_heads<D, BS, true>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s,
+                                 &softmax_stop);
     } else if (warp == kMmaWarp && lane == 0) {
       constexpr uint32_t kIdS = umma_idesc_f16(C::kRows, C::kKeys, 0, 0, BF);
       constexpr uint32_t kIdO = umma_idesc_f16(C::kRows, 2 * D, 0, 1, BF);
@@ -494,18 +539,12 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     const uint32_t obuf = tmem + lane_addr + C::kOCol;
 
     {  // half of the Q row of map g -> shared memory, 128B-swizzled K-major
-      const __half* qrow = a.q + static_cast<int64_t>(tile.row0 + tok) * a.q_stride +
-                           static_cast<int64_t>(2 * head + g) * D;
 #pragma unroll
-      for (int cc = 0; cc < D / 16; ++cc) {
-        const int c = h * (D / 16) + cc;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rv) v = __ldg(reinterpret_cast<const uint4*>(qrow + c * 8));
+      for (int cc = 0; cc < D / 16; ++cc)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                         q_s + g * C::kTileBytes + swz128(r, c)),
-                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         q_s + g * C::kTileBytes + swz128(r, h * (D / 16) + cc)),
+                     "r"(qv[cc].x), "r"(qv[cc].y), "r"(qv[cc].z), "r"(qv[cc].w)
                      : "memory");
-      }
       fence_proxy_async();
       warp_arrive(smem_addr(&q_full));
     }
@@ -640,8 +679,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   __shared__ __align__(8) uint64_t v_full[C::kVStages], v_empty[C::kVStages];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], handed[2][4], pv_done, q_full, drain;
   __shared__ uint32_t tmem_base;
-  __shared__ int warp_count[C::kThreads / 32];
-  __shared__ int chosen_seq, softmax_stop, peer_stop;
+  __shared__ __align__(8) uint64_t rows_in;  // the other map's rows have arrived
+  __shared__ TileScan scan;
+  __shared__ int softmax_stop;
   // [group][half][row]: maximum of the group's latest tile over each half of its columns, in the
   // scores' own unit, rounded up to the upper 24 bits of its float32 (what shared memory is left)
   __shared__ uint16_t max_hi[2][2][C::kRows];
@@ -658,10 +698,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
   Tile tile;
   // both CTAs of the cluster see the same tile: they leave early together or not at all
-  if (!find_tile<BS, C::kThreads>(a, warp_count, &chosen_seq,
-                                  (gridDim.x - 1 - blockIdx.x) / 2, z, split,
-                                  blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
-                                  blockIdx.x == 0 && split == 0, tile))
+  if (!find_tile<BS>(a, scan, (gridDim.x - 1 - blockIdx.x) / 2, z, split,
+                     blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
+                     blockIdx.x == 0 && split == 0, tile))
     return;
   auto cell = [&](int row) {
     return (static_cast<int64_t>(tile.row0 + tile.qbase + row / a.group) * a.num_q_heads +
@@ -673,12 +712,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   auto no_result = [&](int row) {
     if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row)] = -1.f;
   };
-  if (__syncthreads_or(bad_blocks<BS, C::kThreads>(a, tile))) {
-    if (tid == 0) atomicOr(a.err, kErrBlockRange);
-    if (tid < C::kRows) no_result(tid);
-    return;
+  // This thread's share of Q (a quarter of a row), in flight while the barriers are set up.
+  uint4 qv[D / 32];
+  if (warp < C::kSoftmax / 32) {
+    const int r = (warp & 3) * 32 + lane;
+    const bool rv = real_row(r);
+    const __half* qrow =
+        a.q + static_cast<int64_t>(tile.row0 + tile.qbase + (rv ? r / a.group : 0)) * a.q_stride +
+        static_cast<int64_t>(2 * (pair * a.group + r % a.group) + map) * D + (warp >> 2) * (D / 4);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      qv[c] = rv ? __ldg(reinterpret_cast<const uint4*>(qrow) + c) : make_uint4(0u, 0u, 0u, 0u);
   }
-
   if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < C::kKStages; ++i) {
@@ -697,9 +742,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     mbar_init(smem_addr(&pv_done), 1);
     mbar_init(smem_addr(&q_full), C::kSoftmax / 32);
     mbar_init(smem_addr(&drain), 1);
+    mbar_init(smem_addr(&rows_in), 1);
     mbar_init_fence();
     softmax_stop = 0;
-    peer_stop = 1;  // until the peer says otherwise
+    mbar_arrive_expect_tx(smem_addr(&rows_in), 64 * 2 * D * 4);
   }
   tmem_fence_before_sync();
   __syncthreads();
@@ -713,9 +759,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsOther));
     if (warp == kKWarp) {
       stream_heads<D, BS, false>(a, tile, &kmap, 2 * pair + map, 1, C::kKStages, k_full, k_empty,
-                                 k_s);
+                                 k_s, &softmax_stop);
     } else if (warp == kVWarp) {
-      stream_heads<D, BS, true>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s);
+      stream_heads<D, BS, true>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s,
+                                 &softmax_stop);
     } else if (warp == kMmaWarp && lane == 0) {
       constexpr uint32_t kIdS = umma_idesc_f16(C::kRows, C::kKeys, 0, 0, BF);
       constexpr uint32_t kIdO = umma_idesc_f16(C::kRows, 2 * D, 0, 1, BF);
@@ -781,23 +828,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     const uint32_t pair_bar = 1 + g * 4 + quarter;
     const bool rv = real_row(r);
     const int tok = tile.qbase + (rv ? r / a.group : 0);
-    const int head = pair * a.group + r % a.group;
     const int pos = tile.ctx + tok;  // padding rows mirror the tile's first row
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t sbuf = tmem + lane_addr + g * 128;
     const uint32_t obuf = tmem + lane_addr + C::kOCol;
 
     {  // a quarter of the Q row -> shared memory, 128B-swizzled K-major
-      const __half* qrow = a.q + static_cast<int64_t>(tile.row0 + tok) * a.q_stride +
-                           static_cast<int64_t>(2 * head + map) * D;
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         const int c = (g * 2 + h) * (D / 32) + cc;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rv) v = __ldg(reinterpret_cast<const uint4*>(qrow + c * 8));
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                          q_s + (c >> 3) * (C::kRows * 128) + swz128(r, c & 7)),
-                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     "r"(qv[cc].x), "r"(qv[cc].y), "r"(qv[cc].z), "r"(qv[cc].w)
                      : "memory");
       }
       fence_proxy_async();
@@ -907,7 +949,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   const int ch = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;  // softmax warps
   const bool mine = (quarter >> 1) == map, softmax = warp < kKWarp;
   const bool rv = softmax && real_row(r);
-  const int head = pair * a.group + r % a.group;
   const uint32_t obuf = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + C::kOCol;
   const float* red = reinterpret_cast<const float*>(smem);
   const bool ok = !softmax_stop;
@@ -945,83 +986,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
       }
     }
   } else {
-    cluster_sync();  // both CTAs' rings are done with: V's takes the other map's 64 rows
-    // [row of the half][64 chunks of 16 bytes], chunk XORed with the row: conflict-free both ways
+    // Normalised sums -> shared memory, [row of the half][64 chunks of 16 bytes], a chunk's place
+    // XORed with the row (conflict-free both ways): the rows this CTA finishes where K was, the
+    // others in V's second stage, from which one bulk copy takes them to the other CTA's first.
+    cluster_arrive();  // this CTA's tiles are done with
+    const uint32_t own_s = k_s, out_s = v_s + C::kVBytes, in_s = v_s;
     auto chunk_at = [&](uint32_t base, int row, int c) {
       return base + row * (2 * D * 4) + ((c ^ (row & 7)) << 4);
     };
-    if (softmax && !mine) {
-      const uint32_t there = cluster_addr(v_s, map ^ 1);
-      if (ok) {
+    if (softmax && ok) {
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 32) {
-          uint32_t t[32];
-          tmem_ld32(obuf + ch * kCols + c0, t);
-          tmem_wait_ld();
-          tmem_regs_ready(t);
-#pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             chunk_at(there, r & 63, (ch * kCols + c0 + c) / 4)),
-                         "f"(__uint_as_float(t[c]) * inv), "f"(__uint_as_float(t[c + 1]) * inv),
-                         "f"(__uint_as_float(t[c + 2]) * inv), "f"(__uint_as_float(t[c + 3]) * inv)
-                         : "memory");
-        }
-        if (lane == 0 && ch == 0 && (quarter & 1) == 0)
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                           cluster_addr(smem_addr(&peer_stop), map ^ 1)),
-                       "r"(0)
-                       : "memory");
-      }
-    }
-    cluster_sync();
-    if (softmax && mine && ok && !*reinterpret_cast<volatile int*>(&peer_stop)) {
-      const int64_t row = tile.row0 + tile.qbase + (rv ? r / a.group : 0);
-      const float lam = __ldg(a.lam + row * a.lam_stride + head);
-      // 32 columns at a time, once for the row's sum of squares, once for the output (the
-      // registers do not hold 64 columns)
-      auto apart = [&](float own, float other) {
-        return map == 0 ? difference(own, other, lam) : difference(other, own, lam);
-      };
-      auto columns = [&](int c0, float (&y)[32]) {
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
         uint32_t t[32];
-        tmem_ld32(obuf + c0, t);
+        tmem_ld32(obuf + ch * kCols + c0, t);
         tmem_wait_ld();
         tmem_regs_ready(t);
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          float4 p;
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w)
-                       : "r"(chunk_at(v_s, r & 63, (c0 + c) / 4))
+        for (int c = 0; c < 32; c += 4)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           chunk_at(mine ? own_s : out_s, r & 63, (ch * kCols + c0 + c) / 4)),
+                       "f"(__uint_as_float(t[c]) * inv), "f"(__uint_as_float(t[c + 1]) * inv),
+                       "f"(__uint_as_float(t[c + 2]) * inv), "f"(__uint_as_float(t[c + 3]) * inv)
                        : "memory");
-          y[c] = apart(__fmul_rn(__uint_as_float(t[c]), inv), p.x);
-          y[c + 1] = apart(__fmul_rn(__uint_as_float(t[c + 1]), inv), p.y);
-          y[c + 2] = apart(__fmul_rn(__uint_as_float(t[c + 2]), inv), p.z);
-          y[c + 3] = apart(__fmul_rn(__uint_as_float(t[c + 3]), inv), p.w);
-        }
-      };
-      float y[32], sum = 0.f;
-      if (a.norm_w) {
-        float ss = 0.f;
-#pragma unroll 1
-        for (int c0 = 0; c0 < kCols; c0 += 32) {
-          columns(ch * kCols + c0, y);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) ss += y[c] * y[c];
-        }
-        float* sq = reinterpret_cast<float*>(smem) + 6 * C::kRows;
-        sq[ch * C::kRows + r] = ss;
-        asm volatile("bar.sync 10, 256;" ::: "memory");  // the 8 warps of these rows
-        sum = (sq[r] + sq[C::kRows + r]) + (sq[2 * C::kRows + r] + sq[3 * C::kRows + r]);
       }
-      __half* out = a.out + (row * (a.num_q_heads / 2) + head) * (2 * D);
-#pragma unroll 1
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
-        columns(ch * kCols + c0, y);
-        if (rv) finish_columns<D, BF, 32>(a, y, sum, out, out0 + c0);
+      fence_proxy_async();  // the bulk copy reads what these threads wrote
+    }
+    __syncthreads();
+    cluster_wait();  // so are the other CTA's
+    if (tid == 0 && ok)
+      asm volatile(
+          "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+          "[%3];" ::"r"(cluster_addr(in_s, map ^ 1)),
+          "r"(out_s), "r"(64 * 2 * D * 4), "r"(cluster_addr(smem_addr(&rows_in), map ^ 1))
+          : "memory");
+    // A CTA that failed sends nothing: the other one's wait runs out and its rows stay unwritten.
+    if (softmax && ok && __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&rows_in), 0, a.err,
+                                                                 a.wait_limit_ns))) {
+      // eight threads per row, 32 columns each (every eighth chunk)
+      const int row = tid >> 3, sub = tid & 7, rr = 64 * map + row;
+      const bool real = real_row(rr);
+      const int64_t token = tile.row0 + tile.qbase + (real ? rr / a.group : 0);
+      const int dhead = pair * a.group + rr % a.group;
+      const float lam = __ldg(a.lam + token * a.lam_stride + dhead);
+      float y[32], ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float4 x, p;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                     : "r"(chunk_at(own_s, row, i * 8 + sub))
+                     : "memory");
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w)
+                     : "r"(chunk_at(in_s, row, i * 8 + sub))
+                     : "memory");
+        if (map) {
+          const float4 t = x;
+          x = p;
+          p = t;
+        }
+        y[4 * i] = difference(x.x, p.x, lam);
+        y[4 * i + 1] = difference(x.y, p.y, lam);
+        y[4 * i + 2] = difference(x.z, p.z, lam);
+        y[4 * i + 3] = difference(x.w, p.w, lam);
+      }
+      float f = a.out_scale;
+      if (a.norm_w) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) ss += y[i] * y[i];
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        f *= rsqrtf(ss * (1.f / (2 * D)) + a.eps);
+      }
+      __half* out = a.out + (token * (a.num_q_heads / 2) + dhead) * (2 * D);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // O's 64-column pieces are in V's order (half, head); y's: (head, half)
+        const int piece = i >> 1;
+        const int col = ((piece & 1) * 2 + (piece >> 1)) * 64 + ((i & 1) * 8 + sub) * 4;
+        float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (a.norm_w) w = __ldg(reinterpret_cast<const float4*>(a.norm_w + col));
+        if (real)
+          *reinterpret_cast<uint2*>(out + col) =
+              make_uint2(pack2<BF>(y[4 * i] * w.x * f, y[4 * i + 1] * w.y * f),
+                         pack2<BF>(y[4 * i + 2] * w.z * f, y[4 * i + 3] * w.w * f));
       }
     }
+    cluster_sync();  // the copy out of this CTA's shared memory is done
   }
 
   tmem_fence_before_sync();
