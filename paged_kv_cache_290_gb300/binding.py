@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -143,18 +145,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                 ("pa_step_slot_mapping", ctypes.c_int,
                  [I32, PI32, PI32, PI32, I64, I32, I32, PI32, PI64, I64]),
                 ("pa_bm_compact", ctypes.c_int, [VP, I32, PI32, I32, PI32]),
-                ("pa_rope_and_cache", ctypes.c_int,
-                 [P, P, P, P, ctypes.POINTER(PARope), P, P, P, P, S, VP]),
+                ("pa_rope_and_cache", ctypes.c_int, [VP] * 11),
                 ("pa_diff_attention_workspace_size", ctypes.c_size_t,
-                 [I64, I64, I64, I64, I64, ctypes.POINTER(PABatchHint)]),
+                 [I64, I64, I64, I64, I64, VP]),
                 ("pa_diff_attention", ctypes.c_int,
-                 [P, P, P, P, P, P, ctypes.c_float, ctypes.POINTER(PADiff), P,
-                  ctypes.POINTER(PABatchHint), VP, ctypes.c_size_t, VP]),
+                 [VP, VP, VP, VP, VP, VP, ctypes.c_float, VP, VP, VP, VP, ctypes.c_size_t, VP]),
                 ("pa_move_plan_create", VP, [VP, I64, I64]),
                 ("pa_move_plan_destroy", None, [VP]),
                 ("pa_move_plan_staged", I64, [VP]),
-                ("pa_move_blocks_workspace_size", ctypes.c_size_t, [VP, P, I32, I32]),
-                ("pa_move_blocks", ctypes.c_int, [VP, P, P, P, VP, ctypes.c_size_t, VP])):
+                ("pa_move_blocks_workspace_size", ctypes.c_size_t, [VP, VP, I32, I32]),
+                ("pa_move_blocks", ctypes.c_int, [VP, VP, VP, VP, VP, ctypes.c_size_t, VP])):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -253,15 +253,58 @@ def attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scal
     return out
 
 
-def _check_device(*tensors) -> None:
-    """The library runs on the current device and takes device pointers only."""
-    here = torch.cuda.current_device() if all(t.is_cuda for t in tensors) else -1
+# The calls below are made once per layer of a serving step, where a small batch's kernel takes a
+# few microseconds: their descriptors are packed into one buffer per thread, a struct.pack each,
+# instead of ctypes objects field by field (about 1 us a tensor instead of 3).
+_TENSOR_BYTES = ctypes.sizeof(PATensor)
+_PACK_TENSOR = [struct.Struct(f"=Qii{n}q{8 * (5 - n)}x{n}q{8 * (5 - n)}x").pack_into
+                for n in range(6)]
+assert _TENSOR_BYTES == 96
+_PACK_HINT = struct.Struct("=4i")
+_PACK_ROPE = struct.Struct("=iif4xQQ")
+_PACK_DIFF = struct.Struct("=QQff")
+_PACK_SCALES = struct.Struct("=ff")
+_EXTRA = 10 * _TENSOR_BYTES  # where a call's other structs go
+_thread = threading.local()
+
+
+def _buffer():
+    """(buffer, its address) of this thread's packed arguments."""
+    try:
+        return _thread.buffer, _thread.address
+    except AttributeError:
+        _thread.buffer = bytearray(_EXTRA + 128)
+        _thread.address = ctypes.addressof(ctypes.c_char.from_buffer(_thread.buffer))
+        return _thread.buffer, _thread.address
+
+
+def _pack_tensors(buf, tensors) -> int:
+    """Descriptors of ``tensors`` one after the other; the current device, where all must be."""
+    here, at, codes = tensors[0].get_device(), 0, _DTYPES
+    if here < 0 or here != torch.cuda.current_device():
+        raise ValueError(f"every tensor must be on the current CUDA device, got {tensors[0].device}")
     for t in tensors:
-        if not t.is_cuda or t.get_device() != here:
+        if t.get_device() != here:
             raise ValueError(f"every tensor must be on the current CUDA device, got {t.device}")
+        shape = t.shape
+        dim = len(shape)
+        code = codes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        if dim > 5:
+            raise ValueError("rank above 5")
+        _PACK_TENSOR[dim](buf, at, t.data_ptr(), code, dim, *shape, *t.stride())
+        at += 96
+    return here
 
 
-def _workspace(need: int, workspace: Optional[torch.Tensor], device, stream):
+def _raw_stream(stream: Optional[torch.cuda.Stream], device: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _workspace(need: int, workspace: Optional[torch.Tensor], device: int, stream):
     """(tensor, pointer, bytes) of the caller's workspace, or of one allocated here."""
     if workspace is None:
         if need == 0:
@@ -269,8 +312,8 @@ def _workspace(need: int, workspace: Optional[torch.Tensor], device, stream):
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if stream is not None:  # allocated on the current stream, used on another
             workspace.record_stream(stream)
-    else:
-        _check_device(workspace)
+    elif workspace.get_device() != device:
+        raise ValueError(f"every tensor must be on the current CUDA device, got {workspace.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -285,6 +328,11 @@ def rope_axes(sections) -> torch.Tensor:
     return torch.repeat_interleave(torch.arange(len(n), dtype=torch.int32), n)
 
 
+def _check_host_vector(t, dtype, n: int, name: str) -> None:
+    if t.dtype is not dtype or t.is_cuda or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous host {dtype} vector, one entry per pair")
+
+
 def rope_and_cache(q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, q_out=None,
                    axes=None, adjacent: bool = False, factor: float = 1.0, stream=None,
                    k_scale=None, v_scale=None) -> torch.Tensor:
@@ -296,25 +344,30 @@ def rope_and_cache(q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping,
     Pair i is dims (i, i + len(inv_freq)), or (2i, 2i + 1) when ``adjacent``; cos and sin are
     multiplied by ``factor``.  A byte pool is an FP8 (E4M3) cache and needs the two scales."""
     lib = load_library()
-    for name, t, dtype in (("inv_freq", inv_freq, torch.float64), ("axes", axes, torch.int32)):
-        if t is not None and (t.dtype != dtype or t.is_cuda or t.dim() != 1 or
-                              not t.is_contiguous() or t.numel() != inv_freq.numel()):
-            raise ValueError(f"{name} must be a contiguous host {dtype} vector, one entry per pair")
+    pairs = inv_freq.numel()
+    _check_host_vector(inv_freq, torch.float64, pairs, "inv_freq")
+    if axes is not None:
+        _check_host_vector(axes, torch.int32, pairs, "axes")
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if stream is not None:
             q_out.record_stream(stream)
-    _check_device(q, k, v, positions, k_cache, v_cache, slot_mapping, q_out)
     if positions.dim() == 1:
         positions = positions[None]
-    rope = PARope(inv_freq.numel(), int(bool(adjacent)), float(factor), inv_freq.data_ptr(),
-                  axes.data_ptr() if axes is not None else None)
-    sc = None
+    buf, p = _buffer()
+    device = _pack_tensors(buf, (q, k, v, positions, k_cache, v_cache, slot_mapping, q_out))
+    _PACK_ROPE.pack_into(buf, _EXTRA, pairs, 1 if adjacent else 0, factor,
+                         inv_freq.data_ptr(), axes.data_ptr() if axes is not None else 0)
+    scales = None
     if _is_fp8(k_cache):
-        sc = ctypes.byref(PAKVScales(float(k_scale), float(v_scale)))
-    d = [ctypes.byref(describe(x)) for x in (q, k, v, positions, k_cache, v_cache, slot_mapping,
-                                             q_out)]
-    _check(lib.pa_rope_and_cache(*d[:4], ctypes.byref(rope), *d[4:], sc, _stream_handle(stream)))
+        scales = p + _EXTRA + 64
+        _PACK_SCALES.pack_into(buf, _EXTRA + 64, k_scale, v_scale)
+    n = _TENSOR_BYTES
+    status = lib.pa_rope_and_cache(p, p + n, p + 2 * n, p + 3 * n, p + _EXTRA, p + 4 * n,
+                                   p + 5 * n, p + 6 * n, p + 7 * n, scales,
+                                   _raw_stream(stream, device))
+    if status:
+        _check(status)
     return q_out
 
 
@@ -323,7 +376,7 @@ def diff_attention_workspace_size(num_tokens: int, num_seqs: int, num_q_heads: i
                                   max_seq_len: int, num_prefill_seqs: int = 0) -> int:
     hint = PABatchHint(int(max_query_len), int(max_seq_len), int(num_prefill_seqs), 0)
     return int(load_library().pa_diff_attention_workspace_size(
-        num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, ctypes.byref(hint)))
+        num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, ctypes.addressof(hint)))
 
 
 def diff_attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale: float,
@@ -340,22 +393,25 @@ def diff_attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
     its root mean square (``eps`` inside) and multiplied by it; ``out_scale`` multiplies last.
     The other arguments are those of ``attention``."""
     lib = load_library()
-    hint = PABatchHint(int(max_query_len), int(max_seq_len), int(num_prefill_seqs), 0)
-    tensors = [q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, out, lam]
+    tensors = (q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, out, lam)
     if norm_weight is not None:
-        tensors.append(norm_weight)
-    _check_device(*tensors)
+        tensors += (norm_weight,)
+    buf, p = _buffer()
+    device = _pack_tensors(buf, tensors)
+    n, hint, diff = _TENSOR_BYTES, p + _EXTRA, p + _EXTRA + 64
+    _PACK_HINT.pack_into(buf, _EXTRA, max_query_len, max_seq_len, num_prefill_seqs, 0)
+    _PACK_DIFF.pack_into(buf, _EXTRA + 64, p + 7 * n, p + 8 * n if norm_weight is not None else 0,
+                         eps, out_scale)
     need = 0
     if workspace is None and q.dim() == 3 and k_cache.dim() == 4:
-        need = int(lib.pa_diff_attention_workspace_size(
-            q.shape[0], seq_lens.numel(), q.shape[1], k_cache.shape[1], q.shape[2], ctypes.byref(hint)))
-    workspace, wptr, wbytes = _workspace(need, workspace, q.device, stream)
-    d = [describe(x) for x in tensors]
-    diff = PADiff(ctypes.pointer(d[7]), ctypes.pointer(d[8]) if norm_weight is not None else None,
-                  float(eps), float(out_scale))
-    r = [ctypes.byref(x) for x in d[:7]]
-    _check(lib.pa_diff_attention(*r[:6], ctypes.c_float(scale), ctypes.byref(diff), r[6],
-                                 ctypes.byref(hint), wptr, wbytes, _stream_handle(stream)))
+        t, hq, d = q.shape
+        need = lib.pa_diff_attention_workspace_size(t, seq_lens.numel(), hq, k_cache.shape[1], d,
+                                                    hint)
+    workspace, wptr, wbytes = _workspace(need, workspace, device, stream)
+    status = lib.pa_diff_attention(p, p + n, p + 2 * n, p + 3 * n, p + 4 * n, p + 5 * n, scale, diff,
+                                   p + 6 * n, hint, wptr, wbytes, _raw_stream(stream, device))
+    if status:
+        _check(status)
     return out
 
 
@@ -382,8 +438,9 @@ class MovePlan:
         return int(self._lib.pa_move_plan_staged(self._h))
 
     def workspace_size(self, k_cache, layers: int = 1, with_tables: bool = True) -> int:
+        pool = describe(k_cache)
         return int(self._lib.pa_move_blocks_workspace_size(
-            self._h, ctypes.byref(describe(k_cache)), int(layers), int(bool(with_tables))))
+            self._h, ctypes.addressof(pool), int(layers), int(bool(with_tables))))
 
     def close(self):
         if getattr(self, "_h", None):
@@ -405,14 +462,19 @@ def move_blocks(k_cache, v_cache, plan, block_tables=None,
     once as [L, NB, Hkv, bs, d]."""
     lib = load_library()
     if not isinstance(plan, MovePlan):
-        plan = MovePlan(plan, k_cache.shape[k_cache.dim() - 4])
-    tensors = [k_cache, v_cache] + ([block_tables] if block_tables is not None else [])
-    _check_device(*tensors)
-    need = plan.workspace_size(k_cache, 1, block_tables is not None) if workspace is None else 0
-    workspace, wptr, wbytes = _workspace(need, workspace, k_cache.device, stream)
-    d = [ctypes.byref(describe(x)) for x in tensors]
-    _check(lib.pa_move_blocks(plan._h, d[0], d[1], d[2] if block_tables is not None else None,
-                              wptr, wbytes, _stream_handle(stream)))
+        plan = MovePlan(plan, k_cache.shape[-4])
+    buf, p = _buffer()
+    tables = block_tables is not None
+    device = _pack_tensors(buf, (k_cache, v_cache, block_tables) if tables else (k_cache, v_cache))
+    n = _TENSOR_BYTES
+    need = 0
+    if workspace is None:
+        need = lib.pa_move_blocks_workspace_size(plan._h, p, 1, tables)
+    workspace, wptr, wbytes = _workspace(need, workspace, device, stream)
+    status = lib.pa_move_blocks(plan._h, p, p + n, p + 2 * n if tables else None, wptr, wbytes,
+                                _raw_stream(stream, device))
+    if status:
+        _check(status)
 
 
 TIMED_KERNELS = {"decode": 0, "prefill": 1, "shared_prefix": 2}

@@ -548,8 +548,10 @@ cudaError_t launch_rows_t(const DiffArgs& a, const CUtensorMap& kmap, const CUte
                           cudaStream_t stream) {
   using C = RowsCfg<D, NT>;
   auto kern = diff_rows_kernel<D, BS, NT, BF>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::kSmemBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = once_per_device(done, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  });
   if (e != cudaSuccess) return e;
   DiffArgs b = a;
   b.col_groups = (a.verify_rows * a.group + C::kCols - 1) / C::kCols;

@@ -28,6 +28,7 @@
 
 #include "pa_common.cuh"
 #include "pa_diff.h"
+#include "pa_host.h"
 
 namespace pa {
 namespace {
@@ -1082,17 +1083,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
 }
 
 template <typename C, typename K>
-cudaError_t launch_t(K kern, const DiffArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+cudaError_t launch_t(K kern, std::atomic<uint64_t>& done, const DiffArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                      int ctas_per_tile, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::kSmemBytes);
+  cudaError_t e = once_per_device(done, [&] {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           C::kSmemBytes);
+    if (err != cudaSuccess) return err;
+    // setmaxnreg.inc takes registers the CTA was launched with: never launch a build below the
+    // split
+    cudaFuncAttributes attr{};
+    if ((err = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return err;
+    return attr.numRegs * C::kThreads < C::kRegsSoftmax * C::kSoftmax + C::kRegsOther * 128 ||
+                   attr.numRegs * C::kThreads > 65536
+               ? cudaErrorInvalidConfiguration
+               : cudaSuccess;
+  });
   if (e != cudaSuccess) return e;
-  // setmaxnreg.inc takes registers the CTA was launched with: never launch a build below the split
-  cudaFuncAttributes attr{};
-  if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
-  if (attr.numRegs * C::kThreads < C::kRegsSoftmax * C::kSoftmax + C::kRegsOther * 128 ||
-      attr.numRegs * C::kThreads > 65536)
-    return cudaErrorInvalidConfiguration;
   const int tile_q = C::kRows / a.group;
   const dim3 grid(ctas_per_tile * ((a.max_query_len + tile_q - 1) / tile_q), a.num_pairs,
                   a.prefill_seqs * a.key_splits);
@@ -1103,9 +1109,10 @@ cudaError_t launch_t(K kern, const DiffArgs& a, const CUtensorMap& kmap, const C
 template <int BS, bool BF>
 cudaError_t launch_d(const DiffArgs& a, const CUtensorMap& k, const CUtensorMap& v,
                      cudaStream_t st) {
+  static std::atomic<uint64_t> map_done{0}, both_done{0};
   return a.head_dim == 128
-             ? launch_t<MapCfg>(diff_chunk_map_kernel<BS, BF>, a, k, v, 2, st)
-             : launch_t<BothCfg>(diff_chunk_both_kernel<BS, BF>, a, k, v, 1, st);
+             ? launch_t<MapCfg>(diff_chunk_map_kernel<BS, BF>, map_done, a, k, v, 2, st)
+             : launch_t<BothCfg>(diff_chunk_both_kernel<BS, BF>, both_done, a, k, v, 1, st);
 }
 
 }  // namespace

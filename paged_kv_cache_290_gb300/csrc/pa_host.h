@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "pa.h"
@@ -37,6 +38,19 @@ int make_pool_map(CUtensorMap* m, void* base, int64_t rows, int d, int dtype);
 int make_pair_map(CUtensorMap* m, void* base, int64_t tiles, int bs, int d, int dtype);
 
 cudaError_t device_sm_count(int* out);
+
+// Runs `set` once per device for the static `done` it is given (a bit per device): for attributes
+// of a kernel that stay set, whose call costs as much as a small launch.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t>& done, F set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if ((e = set()) == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // A side stream and two events per device and host thread, for work beside the caller's stream.
 struct SideStream {

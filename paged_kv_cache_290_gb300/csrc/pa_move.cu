@@ -29,10 +29,13 @@ namespace pa {
 namespace {
 
 constexpr int kGroup = 8;
-constexpr int kMaxMoves = 1024;  // per launch: 12 KB of the 32 KB of kernel arguments
+// Moves per launch, which travel as kernel arguments: 12 KB of the 32 KB there are.  A short list
+// takes the small size, whose arguments stay below 4 KB (@LAUNCH@).
+constexpr int kMaxMoves = 1024, kFewMoves = 256;
 constexpr int kThreads = 256;
-static_assert(kMaxMoves % kGroup == 0, "a group lies in one launch");
+static_assert(kMaxMoves % kGroup == 0 && kFewMoves % kGroup == 0, "a group lies in one launch");
 
+template <int N>
 struct MoveArgs {
   uint4* k;
   uint4* v;
@@ -45,15 +48,16 @@ struct MoveArgs {
   int32_t* new_ids;
   int32_t* position;
   int base;              // position of this launch's first move
-  int32_t src[kMaxMoves];  // page id, or ~slot of the workspace
-  int32_t dst[kMaxMoves];  // page id, or ~slot
-  int32_t id[kMaxMoves];   // the moved page's old id
+  int32_t src[N];  // page id, or ~slot of the workspace
+  int32_t dst[N];  // page id, or ~slot
+  int32_t id[N];   // the moved page's old id
 };
 
 __device__ __forceinline__ uint4 load_once(const uint4* p) { return __ldcs(p); }
 __device__ __forceinline__ void store_once(uint4* p, const uint4& x) { __stcs(p, x); }
 
-__global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ MoveArgs a) {
+template <int N>
+__global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ MoveArgs<N> a) {
   const int g0 = static_cast<int>(blockIdx.y) * kGroup;
   const int lz = static_cast<int>(blockIdx.z) >> 1, kv = static_cast<int>(blockIdx.z) & 1;
   if (a.position && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x < kGroup) {
@@ -273,53 +277,62 @@ int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
       return fail(PA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   }
-  // as many layers at once as the workspace stages (and a grid's z allows)
+  // as many layers at once as the workspace stages
   int64_t batch = per_layer ? static_cast<int64_t>((workspace_bytes - fixed) / per_layer) : layers;
   batch = std::min<int64_t>(std::max<int64_t>(batch, 1), layers);
-  MoveArgs a;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int32_t* old_ids = tables ? reinterpret_cast<int32_t*>(ws) : nullptr;
   int32_t* new_ids = tables ? reinterpret_cast<int32_t*>(ws + up256(n * sizeof(int32_t))) : nullptr;
   int32_t* position =
       tables ? reinterpret_cast<int32_t*>(ws + 2 * up256(n * sizeof(int32_t))) : nullptr;
-  a.k = static_cast<uint4*>(kl.data);
-  a.v = static_cast<uint4*>(vl.data);
-  a.stage = reinterpret_cast<uint4*>(ws + fixed);
-  a.layer_stride = kstride / per16;
-  a.chunks = page / per16;
-  a.old_ids = old_ids;
-  a.new_ids = new_ids;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  auto launch = [&]() {
-    const dim3 grid(static_cast<unsigned>((a.chunks + kThreads - 1) / kThreads),
-                    static_cast<unsigned>((a.n + kGroup - 1) / kGroup),
-                    static_cast<unsigned>(2 * a.layers));
-    move_kernel<<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  };
   cudaError_t e;
-  for (int64_t l0 = 0; l0 < layers; l0 += batch) {
-    a.layer0 = static_cast<int>(l0);
-    a.layers = static_cast<int>(std::min(batch, layers - l0));
-    a.position = nullptr;
-    const int64_t ns = static_cast<int64_t>(plan->staged.size());
-    for (int64_t b = 0; b < ns; b += kMaxMoves) {
-      a.n = static_cast<int>(std::min<int64_t>(kMaxMoves, ns - b));
-      for (int i = 0; i < a.n; ++i) {
-        a.src[i] = plan->staged[b + i];
-        a.dst[i] = ~static_cast<int32_t>(b + i);
+  auto run = [&](auto& a, int most) -> int {
+    a.k = static_cast<uint4*>(kl.data);
+    a.v = static_cast<uint4*>(vl.data);
+    a.stage = reinterpret_cast<uint4*>(ws + fixed);
+    a.layer_stride = kstride / per16;
+    a.chunks = page / per16;
+    a.old_ids = old_ids;
+    a.new_ids = new_ids;
+    auto launch = [&]() {
+      const dim3 grid(static_cast<unsigned>((a.chunks + kThreads - 1) / kThreads),
+                      static_cast<unsigned>((a.n + kGroup - 1) / kGroup),
+                      static_cast<unsigned>(2 * a.layers));
+      move_kernel<<<grid, kThreads, 0, st>>>(a);
+      return cudaGetLastError();
+    };
+    for (int64_t l0 = 0; l0 < layers; l0 += batch) {
+      a.layer0 = static_cast<int>(l0);
+      a.layers = static_cast<int>(std::min(batch, layers - l0));
+      a.position = nullptr;
+      const int64_t ns = static_cast<int64_t>(plan->staged.size());
+      for (int64_t b = 0; b < ns; b += most) {
+        a.n = static_cast<int>(std::min<int64_t>(most, ns - b));
+        for (int i = 0; i < a.n; ++i) {
+          a.src[i] = plan->staged[b + i];
+          a.dst[i] = ~static_cast<int32_t>(b + i);
+        }
+        if ((e = launch()) != cudaSuccess) return cuda_fail(e, "move_blocks staging launch");
       }
-      if ((e = launch()) != cudaSuccess) return cuda_fail(e, "move_blocks staging launch");
+      a.position = l0 == 0 ? position : nullptr;
+      for (int64_t b = 0; b < n; b += most) {
+        a.n = static_cast<int>(std::min<int64_t>(most, n - b));
+        a.base = static_cast<int>(b);
+        std::copy_n(plan->src.data() + b, a.n, a.src);
+        std::copy_n(plan->dst.data() + b, a.n, a.dst);
+        std::copy_n(plan->id.data() + b, a.n, a.id);
+        if ((e = launch()) != cudaSuccess) return cuda_fail(e, "move_blocks launch");
+      }
     }
-    a.position = l0 == 0 ? position : nullptr;
-    for (int64_t b = 0; b < n; b += kMaxMoves) {
-      a.n = static_cast<int>(std::min<int64_t>(kMaxMoves, n - b));
-      a.base = static_cast<int>(b);
-      std::copy_n(plan->src.data() + b, a.n, a.src);
-      std::copy_n(plan->dst.data() + b, a.n, a.dst);
-      std::copy_n(plan->id.data() + b, a.n, a.id);
-      if ((e = launch()) != cudaSuccess) return cuda_fail(e, "move_blocks launch");
-    }
+    return PA_OK;
+  };
+  if (n <= kFewMoves) {
+    MoveArgs<kFewMoves> a;
+    if ((rc = run(a, kFewMoves))) return rc;
+  } else {
+    MoveArgs<kMaxMoves> a;
+    if ((rc = run(a, kMaxMoves))) return rc;
   }
   if (tables) {
     const int64_t total = block_tables->shape[0] * block_tables->shape[1];
