@@ -12,9 +12,13 @@
 // would be off by a hundredth of a radian at position 10^5.
 //
 // Bound by HBM for long chunks and by the launch for a decode step.  A CTA takes kTokens tokens:
-// its threads first compute the tokens' kTokens * R/2 (cos, sin) into shared memory, one
-// sincospif for all heads, while the first heads' loads are in flight; then a thread keeps its
-// 8 pairs' cos and sin in registers and walks over the heads with 16-byte loads and stores.
+// its threads compute the tokens' kTokens * R/2 (cos, sin) into shared memory, one sincospif for
+// all heads, while their first loads are in flight; then each walks over (token, head)s with two
+// 16-byte loads and stores each, one task's loads in flight while another's is turned.  Four
+// CTAs an SM (64 registers): 8192 tokens of 64 + 8 heads of 128, bf16, 60 us = 5.6 TB/s, 0.84 of
+// the measured copy rate (with 1 / 4 / 8 tokens a CTA 67 / 62 / 66 us; five CTAs of 48
+// registers 76; 128, 384 or 512 threads 60 to 76).  K/V go to scattered slots, 256 bytes each.
+// A decode step of 64 tokens (32 + 8 heads): 2.8 us on the device.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -92,8 +96,16 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
 
 // Rotates the 8 pairs held in chunks x (first) and y (second): first = the a's and second the
 // b's of the half layout; in the adjacent layout chunk x holds pairs 0..3, y pairs 4..7.
-__device__ __forceinline__ void rotate8(float (&x)[8], float (&y)[8], const float (&c)[8],
-                                        const float (&s)[8], bool adjacent) {
+__device__ __forceinline__ void rotate8(float (&x)[8], float (&y)[8], const float* cos8,
+                                        const float* sin8, bool adjacent) {
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 cc = *reinterpret_cast<const float4*>(cos8 + i);
+    const float4 ss = *reinterpret_cast<const float4*>(sin8 + i);
+    c[i] = cc.x, c[i + 1] = cc.y, c[i + 2] = cc.z, c[i + 3] = cc.w;
+    s[i] = ss.x, s[i + 1] = ss.y, s[i + 2] = ss.z, s[i + 3] = ss.w;
+  }
   if (adjacent) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -118,7 +130,7 @@ __device__ __forceinline__ void rotate8(float (&x)[8], float (&y)[8], const floa
 // tokens blockIdx.x * kTokens .. and heads blockIdx.y, blockIdx.y + gridDim.y, ... in units of
 // kSlots heads; heads 0 .. hq-1 are q's, then k's, then v's.
 template <int D, bool BF, bool F8, int kTokens>
-__global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, F8 ? 2 : 4) rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kCols = D / 16, kSlots = kThreads / kCols;
   __shared__ __align__(16) float cos_s[kTokens][kMaxPairs], sin_s[kTokens][kMaxPairs];
   grid_launch_dependents();
@@ -126,90 +138,115 @@ __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const __grid_c
   const int tid = threadIdx.x;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
 
-  for (int i = tid; i < kTokens * a.pairs; i += kThreads) {
-    const int tt = i / a.pairs, p = i % a.pairs;
-    if (t0 + tt < a.num_tokens) {
-      const int64_t pos = a.positions[a.axis[p] * a.pos_stride + t0 + tt];
-      // signed fraction of a turn, times 2^64; in half turns (sincospif's unit): times 2^-63
-      const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * a.turn[p]);
-      float sn, cs;
-      sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn, &cs);
-      cos_s[tt][p] = cs * a.factor;
-      sin_s[tt][p] = sn * a.factor;
-    }
-  }
-  __syncthreads();
-
-  const int col = tid % kCols, slot0 = tid / kCols;
+  const int col = tid % kCols;
   const int rcols = a.pairs / 8;  // columns that rotate
   const bool rot = col < rcols;
   const bool adj = a.adjacent != 0;
-  // the two chunks of this column in a q or k head, and in a v head
+  // the two chunks of this column in a q or k head (in a v head: col and col + kCols)
   const int ch0 = rot ? (adj ? 2 * col : col) : 2 * col;
   const int ch1 = rot ? (adj ? 2 * col + 1 : col + rcols) : 2 * col + 1;
   const int heads = a.hq + 2 * a.hkv;
+  const int here = static_cast<int>(a.num_tokens - t0 < kTokens ? a.num_tokens - t0 : kTokens);
 
-#pragma unroll 1
-  for (int tt = 0; tt < kTokens; ++tt) {
-    const int64_t t = t0 + tt;
-    if (t >= a.num_tokens) break;
-    const int64_t slot = a.slot_mapping[t];
-    const bool keep = slot >= 0 && slot < a.num_slots;
-    if (slot >= a.num_slots && tid == 0 && blockIdx.y == 0) atomicOr(a.err, kErrSlotRange);
-    const int64_t blk = keep ? slot / a.block_size : 0;
-    const int off = keep ? static_cast<int>(slot - blk * a.block_size) : 0;
-    float c[8], s[8];
-    if (rot) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = cos_s[tt][col * 8 + i];
-        s[i] = sin_s[tt][col * 8 + i];
-      }
+  // This thread's (token, head)s, one after the other.
+  struct Task {
+    uint4 w0, w1;
+    int tt, h;     // token of the CTA, head
+    int64_t slot;  // of a k or v head
+    bool write;
+  };
+  int tt = 0, h = tid / kCols + static_cast<int>(blockIdx.y) * kSlots;
+  auto settle = [&] {  // h past the token's heads goes on in the next token
+    while (tt < here && h >= heads) {
+      h -= heads;
+      ++tt;
     }
-    for (int h = slot0 + static_cast<int>(blockIdx.y) * kSlots; h < heads;
-         h += static_cast<int>(gridDim.y) * kSlots) {
-      const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
-      if (!is_q && !keep) continue;
+  };
+  auto load = [&](Task& q) {
+    q.tt = tt;
+    q.h = h;
+    q.write = false;
+    if (tt >= here) return;
+    const int64_t t = t0 + tt;
+    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
+    q.slot = is_q ? 0 : a.slot_mapping[t];
+    q.write = q.slot >= 0 && q.slot < a.num_slots;
+    if (q.write) {
       const int hh = is_q ? h : is_v ? h - a.hq - a.hkv : h - a.hq;
-      const int x0 = is_v ? col : ch0, x1 = is_v ? col + kCols : ch1;
       const __half* src = (is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride
                                                              : a.k + t * a.k_stride) +
                           static_cast<int64_t>(hh) * D;
-      uint4 w0 = *reinterpret_cast<const uint4*>(src + x0 * 8);
-      uint4 w1 = *reinterpret_cast<const uint4*>(src + x1 * 8);
-      const bool turns = rot && !is_v;
-      float x[8], y[8];
-      if (turns || (F8 && !is_q)) {
-        unpack8<BF>(w0, x);
-        unpack8<BF>(w1, y);
-      }
-      if (turns) {
-        rotate8(x, y, c, s, adj);
-        if (!F8 || is_q) {
-          w0 = pack8<BF>(x);
-          w1 = pack8<BF>(y);
-        }
-      }
-      if (is_q) {
-        __half* dst = a.q_out + t * a.qo_stride + static_cast<int64_t>(hh) * D;
-        *reinterpret_cast<uint4*>(dst + x0 * 8) = w0;
-        *reinterpret_cast<uint4*>(dst + x1 * 8) = w1;
-      } else {
-        const int64_t base = ((blk * a.hkv + hh) * a.block_size + off) * D;
-        void* pool = is_v ? a.v_cache : a.k_cache;
-        if constexpr (F8) {
-          // the float32 rotation goes straight to its code: one rounding
-          const float inv = is_v ? a.v_inv : a.k_inv;
-          uint8_t* dst = static_cast<uint8_t*>(pool) + base;
-          *reinterpret_cast<uint2*>(dst + x0 * 8) = codes8(x, inv);
-          *reinterpret_cast<uint2*>(dst + x1 * 8) = codes8(y, inv);
-        } else {
-          __half* dst = static_cast<__half*>(pool) + base;
-          *reinterpret_cast<uint4*>(dst + x0 * 8) = w0;
-          *reinterpret_cast<uint4*>(dst + x1 * 8) = w1;
-        }
+      q.w0 = *reinterpret_cast<const uint4*>(src + (is_v ? col : ch0) * 8);
+      q.w1 = *reinterpret_cast<const uint4*>(src + (is_v ? col + kCols : ch1) * 8);
+    } else if (q.slot >= 0 && h == a.hq && col == 0) {
+      atomicOr(a.err, kErrSlotRange);  // once per token: its first k head
+    }
+    h += static_cast<int>(gridDim.y) * kSlots;
+    settle();
+  };
+  auto finish = [&](Task& q) {
+    if (!q.write) return;
+    const int64_t t = t0 + q.tt;
+    const bool is_q = q.h < a.hq, is_v = q.h >= a.hq + a.hkv;
+    const int hh = is_q ? q.h : is_v ? q.h - a.hq - a.hkv : q.h - a.hq;
+    const int x0 = is_v ? col : ch0, x1 = is_v ? col + kCols : ch1;
+    const bool turns = rot && !is_v;
+    float x[8], y[8];
+    if (turns || (F8 && !is_q)) {
+      unpack8<BF>(q.w0, x);
+      unpack8<BF>(q.w1, y);
+    }
+    if (turns) {
+      rotate8(x, y, &cos_s[q.tt][col * 8], &sin_s[q.tt][col * 8], adj);
+      if (!F8 || is_q) {
+        q.w0 = pack8<BF>(x);
+        q.w1 = pack8<BF>(y);
       }
     }
+    if (is_q) {
+      __half* dst = a.q_out + t * a.qo_stride + static_cast<int64_t>(hh) * D;
+      *reinterpret_cast<uint4*>(dst + x0 * 8) = q.w0;
+      *reinterpret_cast<uint4*>(dst + x1 * 8) = q.w1;
+    } else {
+      const int64_t blk = q.slot / a.block_size;
+      const int off = static_cast<int>(q.slot - blk * a.block_size);
+      const int64_t base = ((blk * a.hkv + hh) * a.block_size + off) * D;
+      void* pool = is_v ? a.v_cache : a.k_cache;
+      if constexpr (F8) {
+        // the float32 rotation goes straight to its code: one rounding
+        const float inv = is_v ? a.v_inv : a.k_inv;
+        uint8_t* dst = static_cast<uint8_t*>(pool) + base;
+        *reinterpret_cast<uint2*>(dst + x0 * 8) = codes8(x, inv);
+        *reinterpret_cast<uint2*>(dst + x1 * 8) = codes8(y, inv);
+      } else {
+        __half* dst = static_cast<__half*>(pool) + base;
+        *reinterpret_cast<uint4*>(dst + x0 * 8) = q.w0;
+        *reinterpret_cast<uint4*>(dst + x1 * 8) = q.w1;
+      }
+    }
+  };
+
+  // Two tasks in turn: one's loads are in flight while the other is turned and stored; the first
+  // one's while the angles are computed.
+  settle();
+  Task even, odd;
+  load(even);
+  for (int i = tid; i < here * a.pairs; i += kThreads) {
+    const int token = i / a.pairs, p = i % a.pairs;
+    const int64_t pos = a.positions[a.axis[p] * a.pos_stride + t0 + token];
+    // signed fraction of a turn, times 2^64; in half turns (sincospif's unit): times 2^-63
+    const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(pos) * a.turn[p]);
+    float sn, cs;
+    sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn, &cs);
+    cos_s[token][p] = cs * a.factor;
+    sin_s[token][p] = sn * a.factor;
+  }
+  __syncthreads();
+  while (even.tt < here) {
+    load(odd);
+    finish(even);
+    load(even);
+    finish(odd);
   }
 }
 
@@ -226,8 +263,8 @@ cudaError_t launch(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (a.num_tokens >= 8 * num_sms) {
-    cfg.gridDim = dim3(static_cast<unsigned>((a.num_tokens + 3) / 4));
-    return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<D, BF, F8, 4>, a);
+    cfg.gridDim = dim3(static_cast<unsigned>((a.num_tokens + 1) / 2));
+    return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<D, BF, F8, 2>, a);
   }
   const int64_t want = (2 * num_sms + a.num_tokens - 1) / a.num_tokens;
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_tokens),
