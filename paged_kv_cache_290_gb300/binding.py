@@ -8,9 +8,8 @@ status.  There is no fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
-import struct
-import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -84,11 +83,12 @@ class PAError(RuntimeError):
 
 
 _lib = None
+_ext = None  # the extension that marshals the per-layer calls
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load (once) the CUDA library; raises if it has not been built."""
-    global _lib
+    global _lib, _ext
     if _lib is None:
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with "
@@ -145,20 +145,31 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                 ("pa_step_slot_mapping", ctypes.c_int,
                  [I32, PI32, PI32, PI32, I64, I32, I32, PI32, PI64, I64]),
                 ("pa_bm_compact", ctypes.c_int, [VP, I32, PI32, I32, PI32]),
-                ("pa_rope_and_cache", ctypes.c_int, [VP] * 11),
+                ("pa_rope_and_cache", ctypes.c_int,
+                 [P, P, P, P, ctypes.POINTER(PARope), P, P, P, P, S, VP]),
                 ("pa_diff_attention_workspace_size", ctypes.c_size_t,
-                 [I64, I64, I64, I64, I64, VP]),
+                 [I64, I64, I64, I64, I64, ctypes.POINTER(PABatchHint)]),
                 ("pa_diff_attention", ctypes.c_int,
-                 [VP, VP, VP, VP, VP, VP, ctypes.c_float, VP, VP, VP, VP, ctypes.c_size_t, VP]),
+                 [P, P, P, P, P, P, ctypes.c_float, ctypes.POINTER(PADiff), P,
+                  ctypes.POINTER(PABatchHint), VP, ctypes.c_size_t, VP]),
                 ("pa_move_plan_create", VP, [VP, I64, I64]),
                 ("pa_move_plan_destroy", None, [VP]),
                 ("pa_move_plan_staged", I64, [VP]),
-                ("pa_move_blocks_workspace_size", ctypes.c_size_t, [VP, VP, I32, I32]),
-                ("pa_move_blocks", ctypes.c_int, [VP, VP, VP, VP, VP, ctypes.c_size_t, VP])):
+                ("pa_move_blocks_workspace_size", ctypes.c_size_t, [VP, P, I32, I32]),
+                ("pa_move_blocks", ctypes.c_int, [VP, P, P, P, VP, ctypes.c_size_t, VP])):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        _lib = lib
+        try:
+            ext = importlib.import_module("._pa_torch", __package__)
+        except ImportError as e:
+            raise RuntimeError("_pa_torch.so is missing or does not fit this torch: build it with "
+                               "`python -m paged_kv_cache_290_gb300.build`") from e
+        ext.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "pa_rope_and_cache", "pa_diff_attention_workspace_size", "pa_diff_attention",
+            "pa_move_plan_create", "pa_move_plan_destroy", "pa_move_blocks_workspace_size",
+            "pa_move_blocks")])
+        _lib, _ext = lib, ext
     return _lib
 
 
@@ -253,70 +264,6 @@ def attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scal
     return out
 
 
-# The calls below are made once per layer of a serving step, where a small batch's kernel takes a
-# few microseconds: their descriptors are packed into one buffer per thread, a struct.pack each,
-# instead of ctypes objects field by field (about 1 us a tensor instead of 3).
-_TENSOR_BYTES = ctypes.sizeof(PATensor)
-_PACK_TENSOR = [struct.Struct(f"=Qii{n}q{8 * (5 - n)}x{n}q{8 * (5 - n)}x").pack_into
-                for n in range(6)]
-assert _TENSOR_BYTES == 96
-_PACK_HINT = struct.Struct("=4i")
-_PACK_ROPE = struct.Struct("=iif4xQQ")
-_PACK_DIFF = struct.Struct("=QQff")
-_PACK_SCALES = struct.Struct("=ff")
-_EXTRA = 10 * _TENSOR_BYTES  # where a call's other structs go
-_thread = threading.local()
-
-
-def _buffer():
-    """(buffer, its address) of this thread's packed arguments."""
-    try:
-        return _thread.buffer, _thread.address
-    except AttributeError:
-        _thread.buffer = bytearray(_EXTRA + 128)
-        _thread.address = ctypes.addressof(ctypes.c_char.from_buffer(_thread.buffer))
-        return _thread.buffer, _thread.address
-
-
-def _pack_tensors(buf, tensors) -> int:
-    """Descriptors of ``tensors`` one after the other; the current device, where all must be."""
-    here, at, codes = tensors[0].get_device(), 0, _DTYPES
-    if here < 0 or here != torch.cuda.current_device():
-        raise ValueError(f"every tensor must be on the current CUDA device, got {tensors[0].device}")
-    for t in tensors:
-        if t.get_device() != here:
-            raise ValueError(f"every tensor must be on the current CUDA device, got {t.device}")
-        shape = t.shape
-        dim = len(shape)
-        code = codes.get(t.dtype)
-        if code is None:
-            raise TypeError(f"unsupported dtype {t.dtype}")
-        if dim > 5:
-            raise ValueError("rank above 5")
-        _PACK_TENSOR[dim](buf, at, t.data_ptr(), code, dim, *shape, *t.stride())
-        at += 96
-    return here
-
-
-def _raw_stream(stream: Optional[torch.cuda.Stream], device: int) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device)
-
-
-def _workspace(need: int, workspace: Optional[torch.Tensor], device: int, stream):
-    """(tensor, pointer, bytes) of the caller's workspace, or of one allocated here."""
-    if workspace is None:
-        if need == 0:
-            return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:  # allocated on the current stream, used on another
-            workspace.record_stream(stream)
-    elif workspace.get_device() != device:
-        raise ValueError(f"every tensor must be on the current CUDA device, got {workspace.device}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
 def rope_inv_freq(rotary_dim: int, base: float = 10000.0) -> torch.Tensor:
     """base^(-2i / rotary_dim) for i < rotary_dim / 2: host float64, as ``rope_and_cache`` takes."""
     return float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
@@ -326,11 +273,6 @@ def rope_axes(sections) -> torch.Tensor:
     """The axis of each pair when axis a takes the next ``sections[a]`` pairs (host int32)."""
     n = torch.as_tensor(list(sections), dtype=torch.int64)
     return torch.repeat_interleave(torch.arange(len(n), dtype=torch.int32), n)
-
-
-def _check_host_vector(t, dtype, n: int, name: str) -> None:
-    if t.dtype is not dtype or t.is_cuda or tuple(t.shape) != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous host {dtype} vector, one entry per pair")
 
 
 def rope_and_cache(q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, q_out=None,
@@ -343,29 +285,15 @@ def rope_and_cache(q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping,
     of each rotated pair, ``axes`` (host int32) the axis each pair turns with (None: axis 0).
     Pair i is dims (i, i + len(inv_freq)), or (2i, 2i + 1) when ``adjacent``; cos and sin are
     multiplied by ``factor``.  A byte pool is an FP8 (E4M3) cache and needs the two scales."""
-    lib = load_library()
-    pairs = inv_freq.numel()
-    _check_host_vector(inv_freq, torch.float64, pairs, "inv_freq")
-    if axes is not None:
-        _check_host_vector(axes, torch.int32, pairs, "axes")
+    if _ext is None:
+        load_library()
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if stream is not None:
+        if stream is not None:  # allocated on the current stream, used on another
             q_out.record_stream(stream)
-    if positions.dim() == 1:
-        positions = positions[None]
-    buf, p = _buffer()
-    device = _pack_tensors(buf, (q, k, v, positions, k_cache, v_cache, slot_mapping, q_out))
-    _PACK_ROPE.pack_into(buf, _EXTRA, pairs, 1 if adjacent else 0, factor,
-                         inv_freq.data_ptr(), axes.data_ptr() if axes is not None else 0)
-    scales = None
-    if _is_fp8(k_cache):
-        scales = p + _EXTRA + 64
-        _PACK_SCALES.pack_into(buf, _EXTRA + 64, k_scale, v_scale)
-    n = _TENSOR_BYTES
-    status = lib.pa_rope_and_cache(p, p + n, p + 2 * n, p + 3 * n, p + _EXTRA, p + 4 * n,
-                                   p + 5 * n, p + 6 * n, p + 7 * n, scales,
-                                   _raw_stream(stream, device))
+    status = _ext.rope(q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, q_out, axes,
+                       adjacent, factor, None if stream is None else stream.cuda_stream, k_scale,
+                       v_scale)
     if status:
         _check(status)
     return q_out
@@ -376,7 +304,7 @@ def diff_attention_workspace_size(num_tokens: int, num_seqs: int, num_q_heads: i
                                   max_seq_len: int, num_prefill_seqs: int = 0) -> int:
     hint = PABatchHint(int(max_query_len), int(max_seq_len), int(num_prefill_seqs), 0)
     return int(load_library().pa_diff_attention_workspace_size(
-        num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, ctypes.addressof(hint)))
+        num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, ctypes.byref(hint)))
 
 
 def diff_attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale: float,
@@ -392,27 +320,26 @@ def diff_attention(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
     [Hq / 2] or [T, Hq / 2].  With ``norm_weight`` (float32 [2d]) each head's result is divided by
     its root mean square (``eps`` inside) and multiplied by it; ``out_scale`` multiplies last.
     The other arguments are those of ``attention``."""
-    lib = load_library()
-    tensors = (q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, out, lam)
-    if norm_weight is not None:
-        tensors += (norm_weight,)
-    buf, p = _buffer()
-    device = _pack_tensors(buf, tensors)
-    n, hint, diff = _TENSOR_BYTES, p + _EXTRA, p + _EXTRA + 64
-    _PACK_HINT.pack_into(buf, _EXTRA, max_query_len, max_seq_len, num_prefill_seqs, 0)
-    _PACK_DIFF.pack_into(buf, _EXTRA + 64, p + 7 * n, p + 8 * n if norm_weight is not None else 0,
-                         eps, out_scale)
-    need = 0
-    if workspace is None and q.dim() == 3 and k_cache.dim() == 4:
-        t, hq, d = q.shape
-        need = lib.pa_diff_attention_workspace_size(t, seq_lens.numel(), hq, k_cache.shape[1], d,
-                                                    hint)
-    workspace, wptr, wbytes = _workspace(need, workspace, device, stream)
-    status = lib.pa_diff_attention(p, p + n, p + 2 * n, p + 3 * n, p + 4 * n, p + 5 * n, scale, diff,
-                                   p + 6 * n, hint, wptr, wbytes, _raw_stream(stream, device))
+    if _ext is None:
+        load_library()
+    if stream is not None and workspace is None:
+        workspace = torch.empty(diff_attention_workspace_size(
+            q.shape[0], seq_lens.numel(), q.shape[1], k_cache.shape[1], q.shape[2], max_query_len,
+            max_seq_len, num_prefill_seqs), dtype=torch.uint8, device=q.device)
+        workspace.record_stream(stream)  # allocated on the current stream, used on another
+    status = _ext.diff(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, lam, out,
+                       max_query_len, max_seq_len, norm_weight, eps, out_scale, workspace,
+                       None if stream is None else stream.cuda_stream, num_prefill_seqs)
     if status:
         _check(status)
     return out
+
+
+def _pairs(pairs) -> torch.Tensor:
+    p = torch.as_tensor(pairs, dtype=torch.int32)
+    if p.is_cuda:
+        raise ValueError("pairs must be on the host")
+    return p.reshape(p.numel() // 2, 2).contiguous()
 
 
 class MovePlan:
@@ -421,10 +348,7 @@ class MovePlan:
     ``move_blocks`` calls may use it."""
 
     def __init__(self, pairs, num_blocks: int):
-        p = torch.as_tensor(pairs, dtype=torch.int32)
-        p = p.reshape(p.numel() // 2, 2).contiguous()
-        if p.is_cuda:
-            raise ValueError("pairs must be on the host")
+        p = _pairs(pairs)
         self._lib = load_library()
         self.num_blocks = int(num_blocks)
         self._h = self._lib.pa_move_plan_create(p.data_ptr() if p.numel() else None, p.shape[0],
@@ -438,9 +362,8 @@ class MovePlan:
         return int(self._lib.pa_move_plan_staged(self._h))
 
     def workspace_size(self, k_cache, layers: int = 1, with_tables: bool = True) -> int:
-        pool = describe(k_cache)
         return int(self._lib.pa_move_blocks_workspace_size(
-            self._h, ctypes.addressof(pool), int(layers), int(bool(with_tables))))
+            self._h, ctypes.byref(describe(k_cache)), int(layers), int(bool(with_tables))))
 
     def close(self):
         if getattr(self, "_h", None):
@@ -460,21 +383,23 @@ def move_blocks(k_cache, v_cache, plan, block_tables=None,
     ``block_tables``.  ``plan`` is a ``MovePlan`` or its pairs (host int32 [n, 2]: src, dst, where
     a destination may be another pair's source); the pools are [NB, Hkv, bs, d], or all layers at
     once as [L, NB, Hkv, bs, d]."""
-    lib = load_library()
-    if not isinstance(plan, MovePlan):
-        plan = MovePlan(plan, k_cache.shape[-4])
-    buf, p = _buffer()
-    tables = block_tables is not None
-    device = _pack_tensors(buf, (k_cache, v_cache, block_tables) if tables else (k_cache, v_cache))
-    n = _TENSOR_BYTES
-    need = 0
-    if workspace is None:
-        need = lib.pa_move_blocks_workspace_size(plan._h, p, 1, tables)
-    workspace, wptr, wbytes = _workspace(need, workspace, device, stream)
-    status = lib.pa_move_blocks(plan._h, p, p + n, p + 2 * n if tables else None, wptr, wbytes,
-                                _raw_stream(stream, device))
+    if _ext is None:
+        load_library()
+    if isinstance(plan, MovePlan):
+        handle = plan._h
+    else:
+        handle = plan if isinstance(plan, torch.Tensor) and plan.dtype == torch.int32 and \
+            not plan.is_cuda and plan.is_contiguous() and plan.dim() == 2 else _pairs(plan)
+    if stream is not None and workspace is None:
+        plan = plan if isinstance(plan, MovePlan) else MovePlan(handle, k_cache.shape[-4])
+        handle = plan._h
+        workspace = torch.empty(plan.workspace_size(k_cache, 1, block_tables is not None),
+                                dtype=torch.uint8, device=k_cache.device)
+        workspace.record_stream(stream)
+    status = _ext.move(handle, k_cache, v_cache, block_tables, workspace,
+                       None if stream is None else stream.cuda_stream)
     if status:
-        _check(status)
+        _check(PA_ERR_INVALID_ARG if status < 0 else status)
 
 
 TIMED_KERNELS = {"decode": 0, "prefill": 1, "shared_prefix": 2}

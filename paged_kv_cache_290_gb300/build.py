@@ -5,13 +5,15 @@ Each .cu file compiles in parallel to an object with
 through nvcc's host compiler); the objects link into
 ``paged_kv_cache_290_gb300/libpa_gb300.so`` with the CUDA runtime linked statically, so the
 library needs only the NVIDIA driver at run time.  ptxas register/spill reports go to
-``_build/ptxas.log``.
+``_build/ptxas.log``.  Beside it, ``_pa_torch.so`` is the Python extension that turns torch tensors
+into the library's descriptors (g++ against torch's headers, no device code).
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa_gb300.so")
+EXT = os.path.join(PKG, "_pa_torch.so")
 SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_prefill.cu", "pa_noalloc.cu",
            "pa_selftest.cu", "pa_block_manager.cpp", "pa_rope.cu", "pa_diff.cu",
            "pa_diff_chunk.cu", "pa_move.cu"]
@@ -41,10 +44,28 @@ def _inputs():
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _build_extension(nvcc: str) -> None:
+    import torch
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths() + [
+        sysconfig.get_paths()["include"], INCLUDE,
+        os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
+    tmp = EXT + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *["-I" + i for i in inc], os.path.join(CSRC, "pa_torch.cpp"), "-o", tmp,
+           *["-L" + d for d in cpp_extension.library_paths()],
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on pa_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -63,8 +84,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        extension = ex.submit(_build_extension, nvcc)
         results = list(ex.map(compile_one, SOURCES))
+        extension.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (_, log), src in zip(results, SOURCES):
             f.write(f"==== {src}\n{log}\n")
