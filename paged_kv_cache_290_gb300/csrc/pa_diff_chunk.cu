@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     } else if (warp == kVWarp) {
       stream_heads<D, BS, true>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s,
                                  &softmax_stop);
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
+      const bool leader = elect_one();
       constexpr uint32_t kIdS = umma_idesc_f16(C::kRows, C::kKeys, 0, 0, BF);
       constexpr uint32_t kIdO = umma_idesc_f16(C::kRows, 2 * D, 0, 1, BF);
       // The pipe queues almost nothing, so a wait between two products idles it for the wait's own
@@ -469,29 +470,32 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
       auto k_bar = [&](int j) { return smem_addr(&k_full[j % C::kKStages]); };
       auto v_bar = [&](int j) { return smem_addr(&v_full[j % C::kVStages]); };
       auto need = [&](bool seen, uint32_t bar, int phase) {
-        const bool ok = seen || mbar_wait_short(bar, phase & 1, a.err, a.wait_limit_ns);
+        const bool ok = seen || __all_sync(0xffffffffu, mbar_wait_short(bar, phase & 1, a.err,
+                                                                        a.wait_limit_ns));
         tmem_fence_after_sync();
         return ok;
       };
       // S_t(j); tests P of the product to follow halfway
       bool p_seen = false, v_seen = false, k_seen = false;
+      auto test = [&](uint32_t bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0;
+      };
       auto issue_s = [&](int t, int j, uint32_t next_p, int next_phase) {
         const uint32_t qb = q_s + t * C::kTileBytes;
         const uint32_t kb = k_s + (j % C::kKStages) * C::kStageBytes + t * C::kTileBytes;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          if (k == D / 16 - 1 && next_phase >= 0) p_seen = mbar_test(next_p, next_phase & 1);
-          umma_f16(tmem + t * 128, umma_sdesc(qb + k * 32, 16, 1024),
+          if (k == D / 16 - 1 && next_phase >= 0) p_seen = test(next_p, next_phase);
+          umma_f16_if(leader, tmem + t * 128, umma_sdesc(qb + k * 32, 16, 1024),
                    umma_sdesc(kb + k * 32, 16, 1024), kIdS, k > 0);
         }
-        umma_commit(smem_addr(&s_full[t]));
+        umma_commit_if(leader, smem_addr(&s_full[t]));
       };
-      bool ok = mbar_wait_short(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) &&
-                need(false, k_bar(0), 0);
+      bool ok = need(false, smem_addr(&q_full), 0) && need(false, k_bar(0), 0);
       if (ok) {
         issue_s(0, 0, 0, -1);
         issue_s(1, 0, 0, -1);
-        umma_commit(smem_addr(&k_empty[0]));
+        umma_commit_if(leader, smem_addr(&k_empty[0]));
       }
       for (int j = 0; ok && j < ntiles; ++j) {
         const int vst = j % C::kVStages;
@@ -507,22 +511,22 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
           for (int k = 0; k < C::kKeys / 16; ++k) {
             if (k == 6 && more) {
               if (t == 0)
-                k_seen = mbar_test(k_bar(j + 1), (j + 1) / C::kKStages & 1);
+                k_seen = test(k_bar(j + 1), (j + 1) / C::kKStages & 1);
               else
-                v_seen = mbar_test(v_bar(j + 1), (j + 1) / C::kVStages & 1);
+                v_seen = test(v_bar(j + 1), (j + 1) / C::kVStages & 1);
             }
-            umma_f16_tmem_a(tmem + C::kOCol + t * 128, tmem + t * 128 + k * 8,
+            umma_f16_tmem_a_if(leader, tmem + C::kOCol + t * 128, tmem + t * 128 + k * 8,
                             umma_sdesc(vb + k * 4096, 2048, 1024), kIdO, (j > 0 || k > 0));
           }
-          if (t == 1) umma_commit(smem_addr(&v_empty[vst]));
+          if (t == 1) umma_commit_if(leader, smem_addr(&v_empty[vst]));
           if (more) {
             if (t == 0) ok = need(k_seen, k_bar(j + 1), (j + 1) / C::kKStages);
             if (ok) issue_s(t, j + 1, smem_addr(&p_full[t ^ 1]), t == 0 ? j : j + 1);
           }
         }
-        if (ok && more) umma_commit(smem_addr(&k_empty[(j + 1) % C::kKStages]));
+        if (ok && more) umma_commit_if(leader, smem_addr(&k_empty[(j + 1) % C::kKStages]));
       }
-      umma_commit(smem_addr(&drain));
+      umma_commit_if(leader, smem_addr(&drain));
       mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
     }
   } else {
@@ -764,33 +768,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     } else if (warp == kVWarp) {
       stream_heads<D, BS, true>(a, tile, &vmap, 2 * pair, 2, C::kVStages, v_full, v_empty, v_s,
                                  &softmax_stop);
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
+      const bool leader = elect_one();
       constexpr uint32_t kIdS = umma_idesc_f16(C::kRows, C::kKeys, 0, 0, BF);
       constexpr uint32_t kIdO = umma_idesc_f16(C::kRows, 2 * D, 0, 1, BF);
       // As in the other kernel: barriers are tested while products still run.
       auto k_bar = [&](int j) { return smem_addr(&k_full[j % C::kKStages]); };
       auto v_bar = [&](int j) { return smem_addr(&v_full[j % C::kVStages]); };
       auto need = [&](bool seen, uint32_t bar, int phase) {
-        const bool ok = seen || mbar_wait_short(bar, phase & 1, a.err, a.wait_limit_ns);
+        const bool ok = seen || __all_sync(0xffffffffu, mbar_wait_short(bar, phase & 1, a.err,
+                                                                        a.wait_limit_ns));
         tmem_fence_after_sync();
         return ok;
       };
       bool p_seen = false, v_seen = false, k_seen = false;
-      auto issue_s = [&](int j, bool test) {  // test: V and P of tile j - 1, the products to follow
+      auto test = [&](uint32_t bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0;
+      };
+      auto issue_s = [&](int j, bool look) {  // look: test V and P of tile j - 1, the products to follow
         const int st = j % C::kKStages;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          if (k == 4 && test) v_seen = mbar_test(v_bar(j - 1), (j - 1) / C::kVStages & 1);
-          if (k == 6 && test) p_seen = mbar_test(smem_addr(&p_full[(j - 1) & 1]), (j - 1) >> 1 & 1);
+          if (k == 4 && look) v_seen = test(v_bar(j - 1), (j - 1) / C::kVStages & 1);
+          if (k == 6 && look) p_seen = test(smem_addr(&p_full[(j - 1) & 1]), (j - 1) >> 1 & 1);
           const uint32_t off = (k >> 2) * (C::kKeys * 128) + (k & 3) * 32;
-          umma_f16(tmem + (j & 1) * 128, umma_sdesc(q_s + off, 16, 1024),
+          umma_f16_if(leader, tmem + (j & 1) * 128, umma_sdesc(q_s + off, 16, 1024),
                    umma_sdesc(k_s + st * C::kTileBytes + off, 16, 1024), kIdS, k > 0);
         }
-        umma_commit(smem_addr(&s_full[j & 1]));
-        umma_commit(smem_addr(&k_empty[st]));
+        umma_commit_if(leader, smem_addr(&s_full[j & 1]));
+        umma_commit_if(leader, smem_addr(&k_empty[st]));
       };
-      bool ok = mbar_wait_short(smem_addr(&q_full), 0, a.err, a.wait_limit_ns) &&
-                need(false, k_bar(0), 0);
+      bool ok = need(false, smem_addr(&q_full), 0) && need(false, k_bar(0), 0);
       if (ok) issue_s(0, false);
       if (ok && ntiles > 1) {
         ok = need(false, k_bar(1), 1 / C::kKStages);
@@ -806,19 +814,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
         const uint32_t vb = v_s + vst * C::kVBytes;
 #pragma unroll
         for (int k = 0; k < C::kKeys / 16; ++k) {
-          if (k == 6 && more) k_seen = mbar_test(k_bar(j + 2), (j + 2) / C::kKStages & 1);
-          umma_f16_tmem_a(tmem + C::kOCol, tmem + (j & 1) * 128 + k * 8,
+          if (k == 6 && more) k_seen = test(k_bar(j + 2), (j + 2) / C::kKStages & 1);
+          umma_f16_tmem_a_if(leader, tmem + C::kOCol, tmem + (j & 1) * 128 + k * 8,
                           umma_sdesc(vb + k * 8192, 2048, 1024), kIdO, (j > 0 || k > 0));
         }
-        umma_commit(smem_addr(&v_empty[vst]));
+        umma_commit_if(leader, smem_addr(&v_empty[vst]));
         if (more) {
           ok = need(k_seen, k_bar(j + 2), (j + 2) / C::kKStages);
           if (ok) issue_s(j + 2, true);
         } else {
-          umma_commit(smem_addr(&pv_done));
+          umma_commit_if(leader, smem_addr(&pv_done));
         }
       }
-      umma_commit(smem_addr(&drain));
+      umma_commit_if(leader, smem_addr(&drain));
       mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
     }
   } else {
