@@ -11,8 +11,9 @@
 //
 // Rows kernel: CTA = (sequence, kv-head pair, partition of the keys).  One read of the four heads'
 // K/V units serves every (query row, head) column of the pair and both maps.  Bound by HBM.
-//   * a warp streams 16-token units (K1, K2, Va, Vb: 4 x 16 x d values) through its own ring of
-//     TMA stages;
+//   * a warp streams 16-token units (K1, K2, Va, Vb: 4 x 16 x d values, two copies) through its
+//     own ring of 2 TMA stages, or 3 or 6 where a small grid leaves the SM's shared memory free
+//     (one sequence of 4096 keys: 17 -> 11 us with the partitions below);
 //   * S^T = K Q^T (m16n8k16: 16 tokens x 8 columns); P^T through movmatrix; O^T += V^T P^T over
 //     2d rows.  NT = 1 packs 4 columns of both maps into one 8-wide tile (columns 0-3 map 1,
 //     4-7 map 2: each K's product with the whole tile, of which its own half is kept, so that one
@@ -37,6 +38,8 @@
 namespace pa {
 namespace {
 
+constexpr int kSms = 152;
+
 template <int D, int NT>
 struct RowsCfg {
   static constexpr int kWarps = D == 128 ? 2 : 4;
@@ -45,16 +48,16 @@ struct RowsCfg {
   static constexpr int kBoxBytes = 16 * 128;
   static constexpr int kHeadBytes = kHalves * kBoxBytes;  // one head's K (or V) of a unit
   static constexpr int kStageBytes = 4 * kHeadBytes;      // K1, K2, Va, Vb
-  static constexpr int kStages = 64 * 1024 / (kWarps * kStageBytes);
-  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kMaxStages = 6;                    // per warp; the launch chooses 2, 3 or 6
+  static_assert(2 * kWarps * kStageBytes == 64 * 1024, "three CTAs of two stages fit an SM");
   static constexpr int kMaxUnits = 64;                    // units of the longest partition
   static constexpr int kDK = D / 16;
   static constexpr int kMT = 2 * D / 16;                  // 16-row tiles of O^T
   static constexpr int kCols = 4 * NT;                    // columns per map
   static constexpr int kMergeBytes = kWarps * 8 * NT * (2 * D + 2) * 4;
-  static constexpr int kSmemBytes = (kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes) + 1024;
+  static constexpr int smem_bytes(int stages) { return kWarps * stages * kStageBytes + 1024; }
+  static_assert(kMergeBytes <= 2 * kWarps * kStageBytes, "the warps' sums fit the rings");
   static constexpr float kRaiseLog2 = 8.f;
-  static_assert(kStages >= 2, "stage ring");
 };
 
 // y of one differential head (kV consecutive dims per lane, a warp per head) -> out.
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
                      const __grid_constant__ CUtensorMap vmap, const DiffArgs a) {
   using C = RowsCfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[C::kWarps][C::kStages];
+  __shared__ __align__(8) uint64_t bars[C::kWarps][C::kMaxStages];
   __shared__ int32_t unit_row[C::kMaxUnits];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -152,8 +155,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
     }
   }
   if (lane == 0) {
-#pragma unroll
-    for (int st = 0; st < C::kStages; ++st) mbar_init(smem_addr(&bars[warp][st]), 1);
+    for (int st = 0; st < a.stages; ++st) mbar_init(smem_addr(&bars[warp][st]), 1);
     mbar_init_fence();
   }
   // A partition without a result says so in its cells (l = -1), and the merge leaves such rows.
@@ -172,11 +174,11 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
   }
 
   const int my_n = warp < nunits ? (nunits - warp + C::kWarps - 1) / C::kWarps : 0;
-  const uint32_t ring = smem_addr(smem + warp * (C::kStages * C::kStageBytes));
+  const int stages = a.stages;
+  const uint32_t ring = smem_addr(smem + warp * stages * C::kStageBytes);
   const uint32_t bar0 = smem_addr(&bars[warp][0]);
   const uint64_t pol = l2_policy_evict_first();  // read once
-  auto issue = [&](int i) {  // lane 0: unit i of this warp into stage i % kStages
-    const int st = i % C::kStages;
+  auto issue = [&](int i, int st) {  // lane 0: unit i of this warp into stage st = i % stages
     const uint32_t bar = bar0 + st * 8;
     const uint32_t dst = ring + st * C::kStageBytes;
     const int y = unit_row[warp + i * C::kWarps];
@@ -187,8 +189,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
   };
   grid_dependency_wait();  // q and the pools now hold what the kernels before wrote
   if (lane == 0) {
-    const int n0 = my_n < C::kStages ? my_n : C::kStages;
-    for (int i = 0; i < n0; ++i) issue(i);
+    for (int i = 0; i < min(my_n, stages); ++i) issue(i, i);
   }
 
   // Q^T as the B operand: n index gq of tile nt is (map, column).
@@ -231,9 +232,9 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
 
   const int mi = lane >> 3, mr = lane & 7;
   int failed_at = -1;
+  int st = 0, phase = 0;  // i % stages, i / stages & 1
   for (int i = 0; i < my_n; ++i) {
-    const int st = i % C::kStages;
-    const bool ok = mbar_wait(bar0 + st * 8, (i / C::kStages) & 1, a.err, a.wait_limit_ns);
+    const bool ok = mbar_wait_short(bar0 + st * 8, phase, a.err, a.wait_limit_ns);
     if (__any_sync(0xffffffffu, !ok)) {
       failed_at = i;
       break;
@@ -336,16 +337,20 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
     }
 
     __syncwarp();
-    if (lane == 0 && i + C::kStages < my_n) {
+    if (lane == 0 && i + stages < my_n) {
       fence_proxy_async();
-      issue(i + C::kStages);
+      issue(i + stages, st);
+    }
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1;
     }
   }
 
   if (failed_at >= 0 && lane == 0) {  // let the copies in flight land before leaving
-    const int issued = min(my_n, failed_at + C::kStages);
+    const int issued = min(my_n, failed_at + stages);
     for (int i = failed_at + 1; i < issued; ++i)
-      mbar_wait(bar0 + (i % C::kStages) * 8, (i / C::kStages) & 1, a.err, a.wait_limit_ns);
+      mbar_wait(bar0 + (i % stages) * 8, (i / stages) & 1, a.err, a.wait_limit_ns);
   }
 
   // ---- join the warps
@@ -431,35 +436,53 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
   }
 }
 
-// Joins n partials (m in log2 units, l, O / l) of one map of one row; a lane holds kV dims.
-// False when one of them says that it has no result (l < 0).
+// Joins n partials (m in log2 units, l, O / l) of one map of one row; a lane holds kV dims.  False
+// when one of them says that it has no result (l < 0).  The first kBatch partials' sums are loaded
+// with all the m and l, before any of them is used.
 template <int kV>
 __device__ __forceinline__ bool join(const float* po, const float* pm, const float* pl, int n,
                                      int lane, float (&y)[kV]) {
-  float M = -INFINITY;
-  bool lost = false;
-  for (int p = lane; p < n; p += 32) {
+  constexpr int kBatch = 8;
+  float4 x[kBatch][kV / 4];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (p0 + i < n) {
+        const float* src = po + static_cast<int64_t>(p0 + i) * (32 * kV) + lane * kV;
+#pragma unroll
+        for (int c = 0; c < kV / 4; ++c) x[i][c] = reinterpret_cast<const float4*>(src)[c];
+      }
+  };
+  float mh = lane < n ? pm[lane] : -INFINITY, lh = lane < n ? pl[lane] : 0.f;  // partial `lane`
+  load(0);
+  float M = mh;
+  bool lost = lh < 0.f;
+  for (int p = lane + 32; p < n; p += 32) {
     M = fmaxf(M, pm[p]);
     lost |= pl[p] < 0.f;
   }
   if (__any_sync(0xffffffffu, lost)) return false;
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float wh = exp2f(mh - M) * lh;
   float wsum = 0.f;
 #pragma unroll
   for (int i = 0; i < kV; ++i) y[i] = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < n; ++p) {
-    const float w = exp2f(pm[p] - M) * pl[p];
-    wsum += w;
-    const float* src = po + static_cast<int64_t>(p) * (32 * kV) + lane * kV;
+  for (int p0 = 0; p0 < n; p0 += kBatch) {
+    if (p0 > 0) load(p0);
 #pragma unroll
-    for (int i = 0; i < kV; i += 4) {
-      const float4 t = *reinterpret_cast<const float4*>(src + i);
-      y[i] += w * t.x;
-      y[i + 1] += w * t.y;
-      y[i + 2] += w * t.z;
-      y[i + 3] += w * t.w;
+    for (int i = 0; i < kBatch; ++i) {
+      const int p = p0 + i;  // the same for every lane
+      if (p >= n) break;
+      const float w = p < 32 ? __shfl_sync(0xffffffffu, wh, p) : exp2f(pm[p] - M) * pl[p];
+      wsum += w;
+#pragma unroll
+      for (int c = 0; c < kV / 4; ++c) {
+        y[4 * c] += w * x[i][c].x;
+        y[4 * c + 1] += w * x[i][c].y;
+        y[4 * c + 2] += w * x[i][c].z;
+        y[4 * c + 3] += w * x[i][c].w;
+      }
     }
   }
   const float inv = 1.f / wsum;
@@ -468,40 +491,52 @@ __device__ __forceinline__ bool join(const float* po, const float* pm, const flo
   return true;
 }
 
-// One warp per (query row, differential head) of the rows kernel: joins both maps' partitions,
-// subtracts, finishes.
+// Two warps per (query row, differential head), one per map: the second map's hands its result
+// over through shared memory, the first one's subtracts and finishes.  All threads of the block
+// call it; `any`: this warp has a row.  c: the row's first partial of this warp's map.
+template <int D, bool BF>
+__device__ __forceinline__ void join_maps(const DiffArgs& a, bool any, const float* po,
+                                          const float* pm, const float* pl, int64_t c, int n,
+                                          int64_t row, int head) {
+  constexpr int kV = 2 * D / 32;
+  __shared__ float other[2][2 * D];
+  __shared__ int lost[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = warp >> 1, map = warp & 1;
+  float y[kV];
+  const bool ok = any && join<kV>(po + c * (2 * D), pm + c, pl + c, n, lane, y);
+  if (map == 1) {
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) other[slot][i * 32 + lane] = y[i];
+    }
+    if (lane == 0) lost[slot] = !ok;
+  }
+  __syncthreads();
+  if (map == 0 && ok && !lost[slot]) {
+    const float lam = __ldg(a.lam + row * a.lam_stride + head);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) y[i] -= lam * other[slot][i * 32 + lane];
+    finish_head<D, BF>(a, y, row, head, lane);
+  }
+}
+
+// Joins the rows kernel's partitions of both maps: two heads a block.
 template <int D, bool BF>
 __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffArgs a) {
   grid_launch_dependents();
-  auto leave = [] { grid_dependency_wait(); };
-  constexpr int kV = 2 * D / 32;
   const int s = blockIdx.y, qi = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = blockIdx.x * 4 + warp;
-  if (head >= a.num_q_heads / 2) return leave();
+  const int map = (threadIdx.x >> 5) & 1;
+  const int head = blockIdx.x * 2 + (threadIdx.x >> 6);
   const int row0 = a.query_start_loc[s], row1 = a.query_start_loc[s + 1];
   const int L = a.seq_lens[s], q_len = row1 - row0;
-  if (q_len < 1 || q_len > a.verify_rows || qi >= q_len || row0 < 0 || row1 > a.num_tokens ||
-      L < q_len)
-    return leave();
   const int nparts = (L + a.part_tokens - 1) / a.part_tokens;
-  if (nparts <= 1 || nparts > a.max_parts || (L + a.block_size - 1) / a.block_size > a.max_blocks)
-    return leave();
+  const bool any = head < a.num_q_heads / 2 && q_len >= 1 && q_len <= a.verify_rows &&
+                   qi < q_len && row0 >= 0 && row1 <= a.num_tokens && L >= q_len && nparts > 1 &&
+                   nparts <= a.max_parts && (L + a.block_size - 1) / a.block_size <= a.max_blocks;
   grid_dependency_wait();
-  const int64_t row = row0 + qi;
-  const int64_t c0 = ((static_cast<int64_t>(s) * a.verify_rows + qi) * a.num_q_heads + 2 * head) *
-                     a.max_parts;
-  float y[2][kV];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const int64_t c = c0 + m * a.max_parts;
-    if (!join<kV>(a.part_o + c * (2 * D), a.part_m + c, a.part_l + c, nparts, lane, y[m])) return;
-  }
-  const float lam = __ldg(a.lam + row * a.lam_stride + head);
-  float z[kV];
-#pragma unroll
-  for (int i = 0; i < kV; ++i) z[i] = y[0][i] - lam * y[1][i];
-  finish_head<D, BF>(a, z, row, head, lane);
+  const int64_t c = ((static_cast<int64_t>(s) * a.verify_rows + qi) * a.num_q_heads + 2 * head +
+                     map) * a.max_parts;
+  join_maps<D, BF>(a, any, a.part_o, a.part_m, a.part_l, c, nparts, row0 + qi, head);
 }
 
 // The same for the chunk kernel's partials: grid y = rank of the chunk's sequence, x over its
@@ -509,38 +544,25 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffArgs a) {
 template <int D, bool BF>
 __global__ void __launch_bounds__(128) diff_chunk_merge_kernel(const DiffArgs a) {
   __shared__ int warp_count[4], chosen_seq;
-  constexpr int kV = 2 * D / 32;
   const int s = find_prefill_seq<128>(a, warp_count, &chosen_seq, blockIdx.y, false);
   if (s < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = a.num_q_heads / 2;
+  const int map = (threadIdx.x >> 5) & 1, heads = a.num_q_heads / 2;
   const int row0 = a.query_start_loc[s], q_len = a.query_start_loc[s + 1] - row0;
   const int L = a.seq_lens[s];
   if (q_len > L || (L + a.block_size - 1) / a.block_size > a.max_blocks || row0 < 0 ||
       row0 + q_len > a.num_tokens || q_len > a.max_query_len || L > a.max_seq_len)
     return;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 2 + (threadIdx.x >> 6);
+  const bool any = i < static_cast<int64_t>(q_len) * heads;
   const int ctx = L - q_len, tile_q = 128 / a.group;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + warp;
-       i < static_cast<int64_t>(q_len) * heads; i += static_cast<int64_t>(gridDim.x) * 4) {
-    const int qi = static_cast<int>(i / heads), head = static_cast<int>(i % heads);
-    const int kend = ctx + min(q_len, (qi / tile_q + 1) * tile_q);
-    const int tiles = (kend + 127) / 128, per = (tiles + a.key_splits - 1) / a.key_splits;
-    const int n = (tiles + per - 1) / per;  // ranges that hold keys
-    const int64_t row = row0 + qi;
-    const int64_t c0 = (row * a.num_q_heads + 2 * head) * a.key_splits;
-    float y[2][kV];
-    bool all = true;
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int64_t c = c0 + m * a.key_splits;
-      all = all && join<kV>(a.chunk_o + c * (2 * D), a.chunk_m + c, a.chunk_l + c, n, lane, y[m]);
-    }
-    if (!all) continue;
-    const float lam = __ldg(a.lam + row * a.lam_stride + head);
-    float z[kV];
-#pragma unroll
-    for (int e = 0; e < kV; ++e) z[e] = y[0][e] - lam * y[1][e];
-    finish_head<D, BF>(a, z, row, head, lane);
-  }
+  const int qi = any ? static_cast<int>(i / heads) : 0, head = static_cast<int>(i % heads);
+  const int kend = ctx + min(q_len, (qi / tile_q + 1) * tile_q);
+  const int tiles = (kend + kChunkKeys - 1) / kChunkKeys;
+  const int per = (tiles + a.key_splits - 1) / a.key_splits;
+  const int n = (tiles + per - 1) / per;  // ranges that hold keys
+  const int64_t row = row0 + qi;
+  const int64_t c = (row * a.num_q_heads + 2 * head + map) * a.key_splits;
+  join_maps<D, BF>(a, any, a.chunk_o, a.chunk_m, a.chunk_l, c, n, row, head);
 }
 
 template <int D, int BS, int NT, bool BF>
@@ -550,15 +572,19 @@ cudaError_t launch_rows_t(const DiffArgs& a, const CUtensorMap& kmap, const CUte
   auto kern = diff_rows_kernel<D, BS, NT, BF>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::smem_bytes(C::kMaxStages));
   });
   if (e != cudaSuccess) return e;
   DiffArgs b = a;
   b.col_groups = (a.verify_rows * a.group + C::kCols - 1) / C::kCols;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.max_parts) * b.col_groups, a.num_pairs, a.num_seqs);
+  // Rings: what the SM's shared memory gives the CTAs that it holds.
+  const int64_t ctas = static_cast<int64_t>(cfg.gridDim.x) * a.num_pairs * a.num_seqs;
+  b.stages = ctas <= kSms ? 6 : ctas <= 2 * kSms ? 3 : 2;
   cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.dynamicSmemBytes = C::smem_bytes(b.stages);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -594,7 +620,7 @@ cudaError_t launch_diff_rows(const DiffArgs& a, const CUtensorMap& kmap, const C
 
 cudaError_t launch_diff_merge(const DiffArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.num_q_heads / 2 + 3) / 4, a.num_seqs, a.verify_rows);
+  cfg.gridDim = dim3((a.num_q_heads / 2 + 1) / 2, a.num_seqs, a.verify_rows);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -611,8 +637,7 @@ cudaError_t launch_diff_merge(const DiffArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_diff_chunk_merge(const DiffArgs& a, cudaStream_t stream) {
   const int64_t work = static_cast<int64_t>(a.max_query_len) * (a.num_q_heads / 2);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((work + 3) / 4, 1 << 20)),
-                  a.prefill_seqs);
+  const dim3 grid(static_cast<unsigned>((work + 1) / 2), a.prefill_seqs);
   if (a.bf16)
     a.head_dim == 128 ? diff_chunk_merge_kernel<128, true><<<grid, 128, 0, stream>>>(a)
                       : diff_chunk_merge_kernel<64, true><<<grid, 128, 0, stream>>>(a);
@@ -645,10 +670,30 @@ DiffPlan diff_plan(int64_t t, int64_t n, int64_t hq, int64_t hkv, int64_t d,
   p.rows_per_seq = p.chunks ? 1 : hint.max_query_len;
   p.prefill_seqs = static_cast<int>(
       hint.num_prefill_seqs > 0 ? std::min<int64_t>(hint.num_prefill_seqs, n) : n);
-  p.part_tokens = 512;
-  p.parts = static_cast<int>(
-      std::max<int64_t>(1, (hint.max_seq_len + int64_t{p.part_tokens} - 1) / p.part_tokens));
+  // Partitions of 128 to 1024 keys: the shortest with which the grid is at most two CTAs an SM, and
+  // 512 where it is more than six even with 1024 (ragged lengths then even out).  Decode steps of
+  // 32 + 8 heads of 128 in us, with partitions of 128 / 256 / 512 / 1024: 1 sequence of 4096 keys
+  // 10.5 / 11.3 / 15.2 / 24.8; 4 of them 22.1 / 16.6 / 18.0 / 25.8; 8: 32.3 / 31.4 / 25.8 / 27.9;
+  // 16: 52.1 / 49.4 / 51.1 / 45.8; 64 of 512 .. 4096 keys 107 / 96.5 / 94.6 / 97.2.
+  const int64_t columns = p.rows_per_seq * group, per_cta = columns <= 4 ? 4 : 8;
+  const int64_t row_ctas = n * (hkv / 2) * ((columns + per_cta - 1) / per_cta);
+  auto parts_of = [&](int64_t tokens) { return (hint.max_seq_len + tokens - 1) / tokens; };
+  p.part_tokens = 128;
+  while (p.part_tokens < 1024 && row_ctas * parts_of(p.part_tokens) > 2 * kSms)
+    p.part_tokens *= 2;
+  if (row_ctas * parts_of(1024) > 6 * kSms) p.part_tokens = 512;
+  p.parts = static_cast<int>(std::max<int64_t>(1, parts_of(p.part_tokens)));
+  // Chunks too few to fill the SMs share out their keys too, 512 at least each, joined by the
+  // merge kernel: a chunk of 32 rows behind 4000 keys (32 + 8 heads of 128) 52 -> 25 us, one of 10
+  // rows (heads of 64) 62 -> 20 us.
   p.key_splits = 1;
+  if (p.chunks) {
+    const int64_t tile_q = 128 / group;
+    const int64_t ctas = (hint.max_query_len + tile_q - 1) / tile_q * (hkv / 2) * p.prefill_seqs *
+                         (d == 128 ? 2 : 1);
+    p.key_splits = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>({kSms / ctas, parts_of(512), 32})));
+  }
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   auto region = [&](size_t bytes) {
     const size_t at = p.total;

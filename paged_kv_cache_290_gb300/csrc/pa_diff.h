@@ -5,6 +5,8 @@
 
 namespace pa {
 
+constexpr int kChunkKeys = 128;  // keys per tile of the chunk kernels
+
 // AttnArgs as in pa_attention (num_q_heads counts both maps' heads; num_kv_heads both maps' keys;
 // group = num_q_heads / num_kv_heads), with `out` [T, Hq / 2, 2 d], and
 struct DiffArgs : AttnArgs {
@@ -15,6 +17,7 @@ struct DiffArgs : AttnArgs {
   float out_scale;
   int part_tokens;       // keys per split-context partition
   int num_pairs;         // num_kv_heads / 2
+  int stages;            // units in flight per warp of the rows kernel
   int max_seq_len;       // the hint's
   int key_splits;        // ranges of the keys that the chunk kernel's CTAs share out
   float* chunk_o;        // partials of the chunk kernel: [T, Hq, key_splits, 2 d]
