@@ -60,6 +60,14 @@ struct RowsCfg {
   static constexpr float kRaiseLog2 = 8.f;
 };
 
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 // y of one differential head (kV consecutive dims per lane, a warp per head) -> out.
 template <int D, bool BF>
 __device__ __forceinline__ void finish_head(const DiffArgs& a, float (&y)[2 * D / 32], int64_t row,
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
           }
         }
     }
-    uint32_t pb0[NT], pb1[NT];
+    uint32_t pb0[NT], pb1[NT], lo0[NT], lo1[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       // a column with no visible key yet is still at m = -inf: subtract 0, so that p = 0, not NaN
@@ -307,10 +315,16 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
       const float p01 = exp2f(sc[nt][1] - b1), p11 = exp2f(sc[nt][3] - b1);
       l_run[nt][0] += p00 + p10;
       l_run[nt][1] += p01 + p11;
-      // P is rounded to the element type for the matrix product: at most 2^-11 (fp16) or 2^-8
-      // (bf16) of each weight, at random over the keys
-      pb0[nt] = movmatrix_trans(pack2<BF>(p00, p01));
-      pb1[nt] = movmatrix_trans(pack2<BF>(p10, p11));
+      // P goes into the matrix product as two element-type numbers, the rounded weight and the
+      // rounded rest: 2^-22 (fp16) or 2^-16 (bf16) of a weight is lost instead of 2^-11 or 2^-8,
+      // which is the output's own rounding, counted twice by the difference of two maps.  The
+      // second product is hidden behind HBM (32 sequences of 8k keys: 167 -> 169 us).
+      const uint32_t h0 = pack2<BF>(p00, p01), h1 = pack2<BF>(p10, p11);
+      const float2 f0 = unpack2<BF>(h0), f1 = unpack2<BF>(h1);
+      pb0[nt] = movmatrix_trans(h0);
+      pb1[nt] = movmatrix_trans(h1);
+      lo0[nt] = movmatrix_trans(pack2<BF>(p00 - f0.x, p01 - f0.y));
+      lo1[nt] = movmatrix_trans(pack2<BF>(p10 - f1.x, p11 - f1.y));
     }
 
     if (nvalid < 16) {  // V rows past the end: p is 0 there, but 0 * NaN is not
@@ -333,7 +347,10 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
       uint32_t af[4];
       ldsm_x4_trans(vb + half * (2 * C::kBoxBytes) + hd * C::kBoxBytes + swz128(tok, chunk & 7), af);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_16816<BF>(o[nt][dt], af, pb0[nt], pb1[nt]);
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_16816<BF>(o[nt][dt], af, pb0[nt], pb1[nt]);
+        mma_16816<BF>(o[nt][dt], af, lo0[nt], lo1[nt]);
+      }
     }
 
     __syncwarp();

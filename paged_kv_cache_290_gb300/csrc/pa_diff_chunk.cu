@@ -84,20 +84,24 @@ struct Tile {
 };
 
 // Finds and checks the tile; false when the CTA has none (errors are reported).  All threads of
-// the block call it.  Grid row z serves the z-th sequence with more than one query row, in batch
-// order: a ballot scan in which every thread also holds its sequence's descriptor, so the chosen
-// one is handed on through shared memory without a second round of loads.
+// the block call it.  Grid row z serves the sequence of rank z among those with more than one
+// query row: longest first while the batch has at most 128 sequences (the longest CTAs then start
+// first and the grid's tail is short: 4 x 512 rows behind 2k to 7.5k keys 206 against 215 us in batch order), else in batch
+// order.  Every thread holds one sequence's descriptor, and the chosen one is handed on through
+// shared memory, without a second round of loads.  keys: 128 words that nothing uses yet (of Q's
+// tile, which only generic stores fill).
 struct TileScan {
   int warp_count[ChunkCfg::kThreads / 32];
   int s, row0, q_len, L;
 };
 template <int BS>
-__device__ __forceinline__ bool find_tile(const DiffArgs& a, TileScan& sc, int qt, int z, int split,
+__device__ __forceinline__ bool find_tile(const DiffArgs& a, TileScan& sc, int* keys, int qt, int z, int split,
                                           bool first, bool lead, Tile& t) {
   constexpr int kThreads = ChunkCfg::kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) sc.s = -1;
   int found = 0;
+  const bool sorted = a.num_seqs <= 128;
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
     const int si = s0 + tid;
     const bool in = si < a.num_seqs;
@@ -108,12 +112,19 @@ __device__ __forceinline__ bool find_tile(const DiffArgs& a, TileScan& sc, int q
     if (a.decode_skipped && first && __any_sync(0xffffffffu, q_len == 1) && lane == 0)
       atomicOr(a.err, kErrHint);
     if (lane == 0) sc.warp_count[warp] = __popc(bal);
+    const int key = q_len > 1 ? max(L, 0) : -1;
+    if (sorted && tid < 128) keys[tid] = key;
     __syncthreads();
     int rank = found + __popc(bal & ((1u << lane) - 1u));
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       rank += w < warp ? sc.warp_count[w] : 0;
       found += sc.warp_count[w];
+    }
+    if (sorted && q_len > 1) {
+      rank = 0;
+      for (int j = 0; j < a.num_seqs; ++j)  // the same word for every thread: a broadcast
+        rank += keys[j] > key || (keys[j] == key && j < tid);
     }
     if (q_len > 1 && rank == z) {
       sc.s = si;
@@ -397,7 +408,7 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   const int pair = blockIdx.y, nsplit = a.key_splits;
   const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
   Tile tile;
-  if (!find_tile<BS>(a, scan, gridDim.x - 1 - blockIdx.x, z, split,
+  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), gridDim.x - 1 - blockIdx.x, z, split,
                      blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
                      blockIdx.x == 0 && split == 0, tile))
     return;
@@ -703,7 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
   Tile tile;
   // both CTAs of the cluster see the same tile: they leave early together or not at all
-  if (!find_tile<BS>(a, scan, (gridDim.x - 1 - blockIdx.x) / 2, z, split,
+  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), (gridDim.x - 1 - blockIdx.x) / 2, z, split,
                      blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
                      blockIdx.x == 0 && split == 0, tile))
     return;
@@ -1000,6 +1011,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     // others in V's second stage, from which one bulk copy takes them to the other CTA's first.
     cluster_arrive();  // this CTA's tiles are done with
     const uint32_t own_s = k_s, out_s = v_s + C::kVBytes, in_s = v_s;
+    // column of y of chunk 8 i + sub: O's 64-column pieces are in V's order (half, head)
+    auto out_column = [](int i, int sub) {
+      const int piece = i >> 1;
+      return ((piece & 1) * 2 + (piece >> 1)) * 64 + ((i & 1) * 8 + sub) * 4;
+    };
     auto chunk_at = [&](uint32_t base, int row, int c) {
       return base + row * (2 * D * 4) + ((c ^ (row & 7)) << 4);
     };
@@ -1021,6 +1037,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
       fence_proxy_async();  // the bulk copy reads what these threads wrote
     }
     __syncthreads();
+    // eight threads per row, 32 columns each (every eighth chunk)
+    const int row = tid >> 3, sub = tid & 7, rr = 64 * map + row;
+    const bool real = softmax && real_row(rr);
+    const int64_t token = tile.row0 + tile.qbase + (real ? rr / a.group : 0);
+    const int dhead = pair * a.group + rr % a.group;
+    const float lam = real ? __ldg(a.lam + token * a.lam_stride + dhead) : 0.f;
     cluster_wait();  // so are the other CTA's
     if (tid == 0 && ok)
       asm volatile(
@@ -1031,12 +1053,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     // A CTA that failed sends nothing: the other one's wait runs out and its rows stay unwritten.
     if (softmax && ok && __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&rows_in), 0, a.err,
                                                                  a.wait_limit_ns))) {
-      // eight threads per row, 32 columns each (every eighth chunk)
-      const int row = tid >> 3, sub = tid & 7, rr = 64 * map + row;
-      const bool real = real_row(rr);
-      const int64_t token = tile.row0 + tile.qbase + (real ? rr / a.group : 0);
-      const int dhead = pair * a.group + rr % a.group;
-      const float lam = __ldg(a.lam + token * a.lam_stride + dhead);
       float y[32], ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -1070,15 +1086,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
       __half* out = a.out + (token * (a.num_q_heads / 2) + dhead) * (2 * D);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        // O's 64-column pieces are in V's order (half, head); y's: (head, half)
-        const int piece = i >> 1;
-        const int col = ((piece & 1) * 2 + (piece >> 1)) * 64 + ((i & 1) * 8 + sub) * 4;
-        float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (a.norm_w) w = __ldg(reinterpret_cast<const float4*>(a.norm_w + col));
+        if (a.norm_w) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(a.norm_w + out_column(i, sub)));
+          y[4 * i] *= w.x;
+          y[4 * i + 1] *= w.y;
+          y[4 * i + 2] *= w.z;
+          y[4 * i + 3] *= w.w;
+        }
         if (real)
-          *reinterpret_cast<uint2*>(out + col) =
-              make_uint2(pack2<BF>(y[4 * i] * w.x * f, y[4 * i + 1] * w.y * f),
-                         pack2<BF>(y[4 * i + 2] * w.z * f, y[4 * i + 3] * w.w * f));
+          *reinterpret_cast<uint2*>(out + out_column(i, sub)) = make_uint2(
+              pack2<BF>(y[4 * i] * f, y[4 * i + 1] * f), pack2<BF>(y[4 * i + 2] * f, y[4 * i + 3] * f));
       }
     }
     cluster_sync();  // the copy out of this CTA's shared memory is done
