@@ -285,6 +285,55 @@ __device__ __forceinline__ float store_weights(uint32_t addr, const uint32_t (&s
   return (s0 + s1) + (s2 + s3);
 }
 
+// A thread's 64 scores from TMEM (scaled where the scale cannot go into the exponent, masked) and
+// their weights 2^(score mul + neg_m), rounded to the element type for the matrix product (at most
+// 2^-11 (fp16) or 2^-8 (bf16) of each weight, at random over the keys), two keys a word.  max: of
+// the scores; returns the unrounded weights' sum.
+template <bool BF>
+__device__ __forceinline__ float weigh(uint32_t addr, uint32_t (&pk)[4][8], float& max,
+                                       bool prescale, float scale_log2, bool masked, int key0,
+                                       int pos, float mul, float neg_m) {
+  uint32_t sv[2][32];
+  tmem_ld32(addr, sv[0]);
+  tmem_ld32(addr + 32, sv[1]);
+  tmem_wait_ld();
+  tmem_regs_ready(sv[0]);
+  tmem_regs_ready(sv[1]);
+  if (prescale || masked) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c) {
+      float v = __uint_as_float(sv[c >> 5][c & 31]);
+      if (prescale) v *= scale_log2;
+      if (masked && key0 + c > pos) v = -INFINITY;
+      sv[c >> 5][c & 31] = __float_as_uint(v);
+    }
+  }
+  const uint64_t mul2 = f32x2(mul, mul), negm2 = f32x2(neg_m, neg_m);
+  uint64_t ps2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+  float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < 64; k += 2) {
+    const float v0 = __uint_as_float(sv[k >> 5][k & 31]);
+    const float v1 = __uint_as_float(sv[k >> 5][(k & 31) + 1]);
+    m2[(k >> 1) & 1] = fmax3(m2[(k >> 1) & 1], v0, v1);
+    float x0, x1;
+    f32x2_split(ffma2(f32x2(v0, v1), mul2, negm2), x0, x1);
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    ps2[(k >> 1) & 1] = fadd2(ps2[(k >> 1) & 1], f32x2(p0, p1));
+    pk[k >> 4][(k & 15) >> 1] = pack2<BF>(p0, p1);
+  }
+  max = fmaxf(m2[0], m2[1]);
+  float s0, s1, s2, s3;
+  f32x2_split(ps2[0], s0, s1);
+  f32x2_split(ps2[1], s2, s3);
+  return (s0 + s1) + (s2 + s3);
+}
+
+// Whether a row's base m gives way to the maximum x (both in the scores' own unit).
+__device__ __forceinline__ bool raises(float m, float x, float mul) {
+  return (x - m) * mul > ChunkCfg::kRescaleLog2 || (m == -INFINITY && x > -INFINITY);
+}
+
 // Columns [0, n) at `addr` of this thread's lane times f.
 __device__ __forceinline__ void rescale(uint32_t addr, int n, float f) {
   for (int c0 = 0; c0 < n; c0 += 16) {
@@ -573,32 +622,47 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
       // S(j) of this map done; it was issued after P V of tile j - 1, so O is settled too
       const bool got = __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&s_full[g]), j & 1, a.err,
                                                                a.wait_limit_ns));
-      uint32_t sv[2][32];
-      float mloc = -INFINITY;
       const int key0 = tile.key_base + j * C::kKeys + h * 64;
-      if (got) {
+      uint32_t pk[4][8];
+      float sum = 0.f;
+      // The weights are taken against the base so far; only when a maximum raises it (the first
+      // tile, rarely later) are they taken again, from the scores still in TMEM.  The maximum and
+      // its exchange are then off the path from S to P (a 4001-row prompt 126 -> 120 us; in the
+      // d = 128 kernel, whose groups pass the base on to each other, the same is slower: 1.17 ->
+      // 1.21 us a tile).
+      for (int turn = 0; turn < 2; ++turn) {
+        float mx = -INFINITY;
+        if (got) {
+          tmem_fence_after_sync();
+          sum = weigh<BF>(sbuf + h * 64, pk, mx, prescale, a.scale_log2,
+                          key0 + 63 > tile.ctx + tile.qbase, key0, pos, mul,
+                          m_run == -INFINITY ? 0.f : -m_run * mul);
+        }
+        half_max[g][h][r] = got ? mx : NAN;  // a maximum itself is never NaN
+        tmem_fence_before_sync();
+        // Both halves have read their scores before either stores P over them.
+        if (!bar_sync_or(pair_bar, 64, !got || raises(m_run, mx, mul))) break;
         tmem_fence_after_sync();
-        mloc = load_scores(sbuf + h * 64, sv, prescale, a.scale_log2,
-                           key0 + 63 > tile.ctx + tile.qbase, key0, pos);
+        const float m0 = half_max[g][0][r], m1 = half_max[g][1][r];
+        if (__any_sync(0xffffffffu, m0 != m0 || m1 != m1)) {  // one of the two has given up
+          stopped = true;
+          break;
+        }
+        mx = fmaxf(m0, m1);
+        float alpha = 1.f;
+        if (raises(m_run, mx, mul)) {
+          alpha = ex2_approx((m_run - mx) * mul);  // 0 when m_run is still -inf
+          m_run = mx;
+          l_run *= alpha;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f))
+          rescale(obuf + g * 128 + h * D, D, alpha);
       }
-      half_max[g][h][r] = mloc;
-      tmem_fence_before_sync();
-      // both halves have read their scores before either stores P over them
-      if (bar_sync_or(pair_bar, 64, !got)) {
-        stopped = true;
-        break;
-      }
+      if (stopped) break;
       tmem_fence_after_sync();
-      const float mx = fmaxf(half_max[g][0][r], half_max[g][1][r]);
-      float alpha = 1.f;
-      if ((mx - m_run) * mul > C::kRescaleLog2 || (m_run == -INFINITY && mx > -INFINITY)) {
-        alpha = ex2_approx((m_run - mx) * mul);  // 0 when m_run is still -inf
-        m_run = mx;
-      }
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f))
-        rescale(obuf + g * 128 + h * D, D, alpha);
-      l_run = l_run * alpha + store_weights<BF>(sbuf + h * 32, sv, mul,
-                                                m_run == -INFINITY ? 0.f : -m_run * mul);
+      l_run += sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_st8(sbuf + h * 32 + i * 8, pk[i]);
       const int tile0 = tile.key_base + j * C::kKeys;
       if (g == 0 && j == ntiles - 1 && tile0 + C::kKeys > tile.key_stop) {
         // V rows past the last visible key may hold any bits: map 0, whose P V comes first,
@@ -877,9 +941,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
       };
       return fmaxf(at(0), at(1));
     };
-    auto raises = [&](float m, float x) {
-      return (x - m) * mul > C::kRescaleLog2 || (m == -INFINITY && x > -INFINITY);
-    };
     for (int j = g; j < ntiles; j += 2) {
       const bool got = __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&s_full[g]), (j >> 1) & 1,
                                                                a.err, a.wait_limit_ns));
@@ -914,9 +975,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
       warp_arrive(smem_addr(&handed[g][quarter]));
       // The base is a function of the maxima so far, so every thread of the row computes the same
       // one: after tile j - 1 (the other group's), then after tile j.
-      const float m_prev = j > 0 && raises(m_run, before) ? before : m_run;
+      const float m_prev = j > 0 && raises(m_run, before, mul) ? before : m_run;
       float m_new = m_prev, alpha = 1.f;
-      if (raises(m_prev, mx)) {
+      if (raises(m_prev, mx, mul)) {
         alpha = ex2_approx((m_prev - mx) * mul);  // 0 when m_prev is -inf
         m_new = mx;
       }
