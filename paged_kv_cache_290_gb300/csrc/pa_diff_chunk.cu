@@ -17,9 +17,10 @@
 //     tiles;
 //   * lane 0 of warp 18 issues the MMAs, P read from TMEM where it overwrote S: the pipe computes
 //     one score buffer's products while the other buffer is in softmax;
-//   * warps 0 .. 15 are the softmax: 256 threads per score buffer, a thread per (row, half of the
-//     tile's columns).  The base m of a row is raised only when a maximum passes it by more
-//     than 2^8 (then O is rescaled in TMEM).
+//   * warps 0 .. 15 are the softmax: all of them take every score buffer in turn, a thread per
+//     (row, quarter of the tile's columns), while the pipe works on the other buffer.  The base m
+//     of a row is raised only when a maximum passes it by more than 2^8 (then O is rescaled in
+//     TMEM).
 // Every wait is bounded; V rows past the last visible key are zeroed before their product.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -37,7 +38,7 @@ namespace {
 // and the softmax warps take 104.
 struct ChunkCfg {
   static constexpr int kRows = 128, kKeys = 128;
-  static constexpr int kSoftmax = 512, kGroup = 256, kThreads = kSoftmax + 128;
+  static constexpr int kSoftmax = 512, kThreads = kSoftmax + 128;
   static constexpr int kRegsSoftmax = 104, kRegsOther = 64, kLaunchRegs = 96;
   static constexpr uint32_t kTmemCols = 512, kOCol = 256;
   static constexpr float kRescaleLog2 = 8.f;
@@ -66,13 +67,6 @@ struct MapCfg : ChunkCfg {                        // d = 128
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-// x rounded up to a float32 whose low 8 bits are 0 (NaN cannot occur: maxima ignore it).
-__device__ __forceinline__ uint32_t round_up24(float x) {
-  const uint32_t u = __float_as_uint(x);
-  if (u & 0x80000000u) return u & 0xffffff00u;  // toward zero is up
-  return u >= 0x7f800000u ? u : (u + 0xffu) & 0xffffff00u;
 }
 
 // The chunk tile of a CTA: its rows and keys.
@@ -227,100 +221,40 @@ __device__ __forceinline__ void stream_heads(const DiffArgs& a, const Tile& t,
       mbar_wait_short(smem_addr(&full[j % stages]), (j / stages) & 1, a.err, a.wait_limit_ns);
 }
 
-// 64 scores of a thread from TMEM, scaled where the scale cannot go into the exponent, masked;
-// returns their maximum.
-__device__ __forceinline__ float load_scores(uint32_t addr, uint32_t (&sv)[2][32], bool prescale,
-                                             float scale_log2, bool masked, int key0, int pos) {
-  tmem_ld32(addr, sv[0]);
-  tmem_ld32(addr + 32, sv[1]);
-  tmem_wait_ld();
-  tmem_regs_ready(sv[0]);
-  tmem_regs_ready(sv[1]);
-  if (prescale || masked) {
-#pragma unroll
-    for (int c = 0; c < 64; ++c) {
-      float v = __uint_as_float(sv[c >> 5][c & 31]);
-      if (prescale) v *= scale_log2;
-      if (masked && key0 + c > pos) v = -INFINITY;
-      sv[c >> 5][c & 31] = __float_as_uint(v);
-    }
-  }
-  float m2[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-  for (int c = 0; c < 64; c += 2)
-    m2[(c >> 1) & 1] = fmax3(m2[(c >> 1) & 1], __uint_as_float(sv[c >> 5][c & 31]),
-                             __uint_as_float(sv[c >> 5][(c & 31) + 1]));
-  return fmaxf(m2[0], m2[1]);
-}
-
-// P = 2^(score mul + neg_m) of the 64 scores -> 32 TMEM columns, two keys each, rounded to the
-// element type for the matrix product (at most 2^-11 (fp16) or 2^-8 (bf16) of each weight, at
-// random over the keys); returns the unrounded weights' sum.  (Summing the rounded weights
-// instead changes the result's error by under 1%.)
-template <bool BF>
-__device__ __forceinline__ float store_weights(uint32_t addr, const uint32_t (&sv)[2][32],
-                                               float mul, float neg_m) {
-  const uint64_t mul2 = f32x2(mul, mul), negm2 = f32x2(neg_m, neg_m);
-  uint64_t ps2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-#pragma unroll
-  for (int q8 = 0; q8 < 4; ++q8) {
-    uint32_t pk[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int k = q8 * 16 + 2 * c;
-      float x0, x1;
-      f32x2_split(ffma2(f32x2(__uint_as_float(sv[k >> 5][k & 31]),
-                              __uint_as_float(sv[k >> 5][(k & 31) + 1])),
-                        mul2, negm2),
-                  x0, x1);
-      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-      ps2[c & 1] = fadd2(ps2[c & 1], f32x2(p0, p1));
-      pk[c] = pack2<BF>(p0, p1);
-    }
-    tmem_st8(addr + q8 * 8, pk);
-  }
-  float s0, s1, s2, s3;
-  f32x2_split(ps2[0], s0, s1);
-  f32x2_split(ps2[1], s2, s3);
-  return (s0 + s1) + (s2 + s3);
-}
-
-// A thread's 64 scores from TMEM (scaled where the scale cannot go into the exponent, masked) and
+// A thread's 32 scores from TMEM (scaled where the scale cannot go into the exponent, masked) and
 // their weights 2^(score mul + neg_m), rounded to the element type for the matrix product (at most
 // 2^-11 (fp16) or 2^-8 (bf16) of each weight, at random over the keys), two keys a word.  max: of
-// the scores; returns the unrounded weights' sum.
+// the scores; returns the unrounded weights' sum.  (Summing the rounded weights instead changes the
+// result's error by under 1%.)
 template <bool BF>
-__device__ __forceinline__ float weigh(uint32_t addr, uint32_t (&pk)[4][8], float& max,
-                                       bool prescale, float scale_log2, bool masked, int key0,
-                                       int pos, float mul, float neg_m) {
-  uint32_t sv[2][32];
-  tmem_ld32(addr, sv[0]);
-  tmem_ld32(addr + 32, sv[1]);
+__device__ __forceinline__ float weigh(uint32_t addr, uint32_t (&pk)[16], float& max, bool prescale,
+                                       float scale_log2, bool masked, int key0, int pos, float mul,
+                                       float neg_m) {
+  uint32_t sv[32];
+  tmem_ld32(addr, sv);
   tmem_wait_ld();
-  tmem_regs_ready(sv[0]);
-  tmem_regs_ready(sv[1]);
+  tmem_regs_ready(sv);
   if (prescale || masked) {
 #pragma unroll
-    for (int c = 0; c < 64; ++c) {
-      float v = __uint_as_float(sv[c >> 5][c & 31]);
+    for (int c = 0; c < 32; ++c) {
+      float v = __uint_as_float(sv[c]);
       if (prescale) v *= scale_log2;
       if (masked && key0 + c > pos) v = -INFINITY;
-      sv[c >> 5][c & 31] = __float_as_uint(v);
+      sv[c] = __float_as_uint(v);
     }
   }
   const uint64_t mul2 = f32x2(mul, mul), negm2 = f32x2(neg_m, neg_m);
   uint64_t ps2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
   float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-  for (int k = 0; k < 64; k += 2) {
-    const float v0 = __uint_as_float(sv[k >> 5][k & 31]);
-    const float v1 = __uint_as_float(sv[k >> 5][(k & 31) + 1]);
+  for (int k = 0; k < 32; k += 2) {
+    const float v0 = __uint_as_float(sv[k]), v1 = __uint_as_float(sv[k + 1]);
     m2[(k >> 1) & 1] = fmax3(m2[(k >> 1) & 1], v0, v1);
     float x0, x1;
     f32x2_split(ffma2(f32x2(v0, v1), mul2, negm2), x0, x1);
     const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
     ps2[(k >> 1) & 1] = fadd2(ps2[(k >> 1) & 1], f32x2(p0, p1));
-    pk[k >> 4][(k & 15) >> 1] = pack2<BF>(p0, p1);
+    pk[k >> 1] = pack2<BF>(p0, p1);
   }
   max = fmaxf(m2[0], m2[1]);
   float s0, s1, s2, s3;
@@ -347,16 +281,81 @@ __device__ __forceinline__ void rescale(uint32_t addr, int n, float f) {
   }
 }
 
-// Clears row r of head h of a V tile (whole 128-byte rows, so the swizzle does not matter).
+// Clears 64 columns (`half`) of row r of head h of a V tile (a whole 128-byte row of it, so the
+// swizzle does not matter).
 template <int kHalves>
-__device__ __forceinline__ void clear_v_row(uint32_t tile, int r, int h) {
-  const uint32_t row = tile + (r >> 4) * (2 * kHalves * 2048) + h * 2048 + (r & 15) * 128;
+__device__ __forceinline__ void clear_v_row(uint32_t tile, int r, int half, int h) {
+  const uint32_t row =
+      tile + (r >> 4) * (2 * kHalves * 2048) + half * 4096 + h * 2048 + (r & 15) * 128;
 #pragma unroll
-  for (int c = 0; c < kHalves * 8; ++c)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + (c >> 3) * 4096 +
-                                                                  (c & 7) * 16),
-                 "r"(0u)
+  for (int c = 0; c < 8; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + c * 16), "r"(0u)
                  : "memory");
+}
+
+// x rounded up to a float32 whose low 8 bits are 0 (NaN cannot occur: maxima ignore it).
+__device__ __forceinline__ uint32_t round_up24(float x) {
+  const uint32_t u = __float_as_uint(x);
+  if (u & 0x80000000u) return u & 0xffffff00u;  // toward zero is up
+  return u >= 0x7f800000u ? u : (u + 0xffu) & 0xffffff00u;
+}
+
+// Shared maxima of a tile: [column quarter][row], the upper 24 bits of a float32 rounded up, in
+// two arrays (what shared memory the d = 128 kernel has left).
+struct Maxima {
+  uint16_t hi[4][ChunkCfg::kRows];
+  uint8_t lo[4][ChunkCfg::kRows];
+};
+
+// One score buffer's softmax by the 512 threads: this thread's row r, columns 32 cq .. + 31 of S at
+// sbuf.  The weights are taken against the row's base m so far; only when a maximum raises it (the
+// first tile, rarely later) are they taken again, from the scores still in TMEM, after `rebase` has
+// brought O to the new base.  So the maxima and their exchange are off the path from S to P; the
+// one meeting of the row's four threads only asks whether anyone raises.  P goes where the
+// thread's own scores were: 16 columns from 32 cq on.  False, for all four of a row's warps, when one
+// of them had no scores (its wait gave up).
+template <bool BF, typename Rebase>
+__device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int r, int cq,
+                                       uint32_t meet_bar, bool prescale, float scale_log2,
+                                       bool masked, int key0, int pos, float mul, float& m_run,
+                                       float& l_run, Rebase rebase) {
+  uint32_t pk[16];
+  float sum = 0.f;
+  for (int turn = 0; turn < 2; ++turn) {
+    uint32_t up = 0x7fffff00u;  // NaN: this thread has given up (a maximum itself is never NaN)
+    if (got) {
+      float top;
+      tmem_fence_after_sync();
+      sum = weigh<BF>(sbuf + 32 * cq, pk, top, prescale, scale_log2, masked, key0, pos, mul,
+                      m_run == -INFINITY ? 0.f : -m_run * mul);
+      up = round_up24(top);
+    }
+    mx.hi[cq][r] = static_cast<uint16_t>(up >> 16);
+    mx.lo[cq][r] = static_cast<uint8_t>(up >> 8);
+    tmem_fence_before_sync();
+    if (!bar_sync_or(meet_bar, 128, !got || raises(m_run, __uint_as_float(up), mul))) break;
+    tmem_fence_after_sync();
+    float top = -INFINITY;
+    bool lost = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t hi = mx.hi[i][r];
+      lost |= hi == 0x7fffu;
+      top = fmaxf(top, __uint_as_float(hi << 16 | static_cast<uint32_t>(mx.lo[i][r]) << 8));
+    }
+    if (__any_sync(0xffffffffu, lost)) return false;
+    float alpha = 1.f;
+    if (raises(m_run, top, mul)) {
+      alpha = ex2_approx((m_run - top) * mul);  // 0 when m_run is still -inf
+      m_run = top;
+      l_run *= alpha;
+    }
+    if (__any_sync(0xffffffffu, alpha != 1.f)) rebase(alpha);
+  }
+  tmem_fence_after_sync();
+  l_run += sum;
+  tmem_st16(sbuf + 32 * cq, pk);
+  return true;
 }
 
 __device__ __forceinline__ void alloc_tmem(uint32_t* base, uint32_t cols) {  // one warp
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ TileScan scan;
   __shared__ int softmax_stop;
-  __shared__ float half_max[2][2][C::kRows];  // [map][half][row], of the latest tile
+  __shared__ Maxima maxima[2];  // per map
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -473,17 +472,20 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   auto no_result = [&](int row, int map) {
     if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row, map)] = -1.f;
   };
-  // This thread's share of Q (half a row of its map), in flight while the barriers are set up.
-  uint4 qv[D / 16];
+  // This thread's share of Q (a quarter of each map's row), in flight while the barriers are set up.
+  uint4 qv[2][D / 32];
   if (warp < C::kSoftmax / 32) {
-    const int r = (warp & 3) * 32 + lane, h = (warp >> 2) & 1, g = warp >> 3;
+    const int r = (warp & 3) * 32 + lane;
     const bool rv = real_row(r);
     const __half* qrow =
         a.q + static_cast<int64_t>(tile.row0 + tile.qbase + (rv ? r / a.group : 0)) * a.q_stride +
-        static_cast<int64_t>(2 * (pair * a.group + r % a.group) + g) * D + h * (D / 2);
+        static_cast<int64_t>(2 * (pair * a.group + r % a.group)) * D + (warp >> 2) * (D / 4);
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c)
-      qv[c] = rv ? __ldg(reinterpret_cast<const uint4*>(qrow) + c) : make_uint4(0u, 0u, 0u, 0u);
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+        qv[t][c] = rv ? __ldg(reinterpret_cast<const uint4*>(qrow + t * D) + c)
+                      : make_uint4(0u, 0u, 0u, 0u);
   }
   if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
   if (tid == 0) {
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
-      mbar_init(smem_addr(&p_full[i]), C::kGroup / 32);
+      mbar_init(smem_addr(&p_full[i]), C::kSoftmax / 32);
     }
     mbar_init(smem_addr(&q_full), C::kSoftmax / 32);
     mbar_init(smem_addr(&drain), 1);
@@ -575,7 +577,8 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
               else
                 v_seen = test(v_bar(j + 1), (j + 1) / C::kVStages & 1);
             }
-            umma_f16_tmem_a_if(leader, tmem + C::kOCol + t * 128, tmem + t * 128 + k * 8,
+            umma_f16_tmem_a_if(leader, tmem + C::kOCol + t * 128,
+                               tmem + t * 128 + (k >> 1) * 32 + (k & 1) * 8,
                             umma_sdesc(vb + k * 4096, 2048, 1024), kIdO, (j > 0 || k > 0));
           }
           if (t == 1) umma_commit_if(leader, smem_addr(&v_empty[vst]));
@@ -590,95 +593,65 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
       mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
     }
   } else {
-    // ================================================ softmax: 256 threads per map
+    // ================================================ softmax: both maps' tiles in turn
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    const int g = warp >> 3, h = (warp >> 2) & 1, quarter = warp & 3;
+    const int cq = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // TMEM lane = row of the tile
-    const uint32_t pair_bar = 1 + g * 4 + quarter;
     const bool rv = real_row(r);
     const int tok = tile.qbase + (rv ? r / a.group : 0);
     const int head = pair * a.group + r % a.group;
     const int pos = tile.ctx + tok;  // padding rows mirror the tile's first row
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t sbuf = tmem + lane_addr + g * 128;
     const uint32_t obuf = tmem + lane_addr + C::kOCol;
 
-    {  // half of the Q row of map g -> shared memory, 128B-swizzled K-major
+    // Q -> shared memory, 128B-swizzled K-major
 #pragma unroll
-      for (int cc = 0; cc < D / 16; ++cc)
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                         q_s + g * C::kTileBytes + swz128(r, h * (D / 16) + cc)),
-                     "r"(qv[cc].x), "r"(qv[cc].y), "r"(qv[cc].z), "r"(qv[cc].w)
+                         q_s + t * C::kTileBytes + swz128(r, cq * (D / 32) + c)),
+                     "r"(qv[t][c].x), "r"(qv[t][c].y), "r"(qv[t][c].z), "r"(qv[t][c].w)
                      : "memory");
-      fence_proxy_async();
-      warp_arrive(smem_addr(&q_full));
-    }
+    fence_proxy_async();
+    warp_arrive(smem_addr(&q_full));
 
     bool stopped = false;
-    float m_run = -INFINITY, l_run = 0.f;  // m in the scores' unit
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};  // m in the scores' unit
     const bool prescale = !(a.scale_log2 > 0.f);
     const float mul = prescale ? 1.f : a.scale_log2;
-    for (int j = 0; j < ntiles; ++j) {
-      // S(j) of this map done; it was issued after P V of tile j - 1, so O is settled too
-      const bool got = __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&s_full[g]), j & 1, a.err,
-                                                               a.wait_limit_ns));
-      const int key0 = tile.key_base + j * C::kKeys + h * 64;
-      uint32_t pk[4][8];
-      float sum = 0.f;
-      // The weights are taken against the base so far; only when a maximum raises it (the first
-      // tile, rarely later) are they taken again, from the scores still in TMEM.  The maximum and
-      // its exchange are then off the path from S to P (a 4001-row prompt 126 -> 120 us; in the
-      // d = 128 kernel, whose groups pass the base on to each other, the same is slower: 1.17 ->
-      // 1.21 us a tile).
-      for (int turn = 0; turn < 2; ++turn) {
-        float mx = -INFINITY;
-        if (got) {
-          tmem_fence_after_sync();
-          sum = weigh<BF>(sbuf + h * 64, pk, mx, prescale, a.scale_log2,
-                          key0 + 63 > tile.ctx + tile.qbase, key0, pos, mul,
-                          m_run == -INFINITY ? 0.f : -m_run * mul);
-        }
-        half_max[g][h][r] = got ? mx : NAN;  // a maximum itself is never NaN
-        tmem_fence_before_sync();
-        // Both halves have read their scores before either stores P over them.
-        if (!bar_sync_or(pair_bar, 64, !got || raises(m_run, mx, mul))) break;
-        tmem_fence_after_sync();
-        const float m0 = half_max[g][0][r], m1 = half_max[g][1][r];
-        if (__any_sync(0xffffffffu, m0 != m0 || m1 != m1)) {  // one of the two has given up
-          stopped = true;
+    for (int j = 0; j < ntiles && !stopped; ++j) {
+      const int key0 = tile.key_base + j * C::kKeys + cq * 32;
+      const bool masked = key0 + 31 > tile.ctx + tile.qbase;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        // S(j) of this map done; it was issued after P V of tile j - 1, so O is settled too
+        const bool got = __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&s_full[t]), j & 1,
+                                                                 a.err, a.wait_limit_ns));
+        auto rebase = [&](float alpha) {
+          if (j > 0) rescale(obuf + t * 128 + cq * (D / 2), D / 2, alpha);
+        };
+        if (!soften<BF>(tmem + lane_addr + t * 128, got, maxima[t], r, cq, 1 + quarter, prescale,
+                        a.scale_log2, masked, key0, pos, mul, m_run[t], l_run[t], rebase)) {
+          stopped = true;  // the row's four warps leave together
           break;
         }
-        mx = fmaxf(m0, m1);
-        float alpha = 1.f;
-        if (raises(m_run, mx, mul)) {
-          alpha = ex2_approx((m_run - mx) * mul);  // 0 when m_run is still -inf
-          m_run = mx;
-          l_run *= alpha;
+        const int tile0 = tile.key_base + j * C::kKeys;
+        if (t == 0 && j == ntiles - 1 && tile0 + C::kKeys > tile.key_stop) {
+          // V rows past the last visible key may hold any bits: they are cleared before the first
+          // product of their tile, once it has landed (row r of head cq per thread)
+          const int vst = j % C::kVStages;
+          if (!mbar_wait_short(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err,
+                               a.wait_limit_ns))
+            softmax_stop = 1;  // no row is written
+          else if (cq < 2 && tile0 + r >= tile.key_stop)
+            clear_v_row<1>(v_s + vst * C::kStageBytes, r, 0, cq);
+          fence_proxy_async();
         }
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f))
-          rescale(obuf + g * 128 + h * D, D, alpha);
+        tmem_wait_st();
+        tmem_fence_before_sync();
+        warp_arrive(smem_addr(&p_full[t]));
       }
-      if (stopped) break;
-      tmem_fence_after_sync();
-      l_run += sum;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_st8(sbuf + h * 32 + i * 8, pk[i]);
-      const int tile0 = tile.key_base + j * C::kKeys;
-      if (g == 0 && j == ntiles - 1 && tile0 + C::kKeys > tile.key_stop) {
-        // V rows past the last visible key may hold any bits: map 0, whose P V comes first,
-        // clears them once the tile has landed (row r of head h per thread)
-        const int vst = j % C::kVStages;
-        if (!mbar_wait_short(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err,
-                             a.wait_limit_ns))
-          stopped = true;
-        else if (tile0 + r >= tile.key_stop)
-          clear_v_row<1>(v_s + vst * C::kStageBytes, r, h);
-        fence_proxy_async();
-      }
-      tmem_wait_st();
-      tmem_fence_before_sync();
-      // a warp that gave up hands over nothing; its pair leaves at the next tile's meeting
-      if (!__any_sync(0xffffffffu, stopped)) warp_arrive(smem_addr(&p_full[g]));
     }
 
     // ---- the row's sums of both maps; every softmax thread meets here
@@ -688,24 +661,28 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     if (!ok) softmax_stop = 1;
     softmax_sync();
     ok = !*reinterpret_cast<volatile int*>(&softmax_stop);
-    if (ok) red[(g * 2 + h) * C::kRows + r] = l_run;
+    if (ok) {
+      red[cq * C::kRows + r] = l_run[0];
+      red[(4 + cq) * C::kRows + r] = l_run[1];
+    }
     softmax_sync();
     if (!ok) {
-      if (h == 0) no_result(r, g);
+      if (cq < 2) no_result(r, cq);
     } else {
       tmem_fence_after_sync();
       float inv[2];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const float l = red[2 * m * C::kRows + r] + red[(2 * m + 1) * C::kRows + r];
+        const float* p = red + 4 * m * C::kRows + r;
+        const float l = (p[0] + p[C::kRows]) + (p[2 * C::kRows] + p[3 * C::kRows]);
         inv[m] = l > 0.f ? 1.f / l : 0.f;  // 0: the row sees no key of this range
-        if (nsplit > 1 && rv && h == 0 && g == m) {
-          a.chunk_m[cell(r, m)] = m_run * mul;
+        if (nsplit > 1 && rv && cq == m) {
+          a.chunk_m[cell(r, m)] = m_run[m] * mul;
           a.chunk_l[cell(r, m)] = l;
         }
       }
       constexpr int kCols = 2 * D / 4;  // this thread's columns of y
-      const int col0 = (g * 2 + h) * kCols;
+      const int col0 = cq * kCols;
       uint32_t o0[kCols], o1[kCols];
       tmem_ld32(obuf + col0, o0);
       tmem_ld32(obuf + 128 + col0, o1);
@@ -730,8 +707,8 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
                             __fmul_rn(__uint_as_float(o1[c]), inv[1]), lam);
           ss += y[c] * y[c];
         }
-        float* sq = red + 4 * C::kRows;
-        sq[(g * 2 + h) * C::kRows + r] = ss;
+        float* sq = red + 8 * C::kRows;
+        sq[cq * C::kRows + r] = ss;
         softmax_sync();
         const float sum = (sq[r] + sq[C::kRows + r]) + (sq[2 * C::kRows + r] + sq[3 * C::kRows + r]);
         if (rv)
@@ -757,15 +734,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t k_full[C::kKStages], k_empty[C::kKStages];
   __shared__ __align__(8) uint64_t v_full[C::kVStages], v_empty[C::kVStages];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], handed[2][4], pv_done, q_full, drain;
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done, q_full, drain;
   __shared__ uint32_t tmem_base;
   __shared__ __align__(8) uint64_t rows_in;  // the other map's rows have arrived
   __shared__ TileScan scan;
   __shared__ int softmax_stop;
-  // [group][half][row]: maximum of the group's latest tile over each half of its columns, in the
-  // scores' own unit, rounded up to the upper 24 bits of its float32 (what shared memory is left)
-  __shared__ uint16_t max_hi[2][2][C::kRows];
-  __shared__ uint8_t max_lo[2][2][C::kRows];
+  __shared__ Maxima maxima;
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -816,8 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&s_full[i]), 1);
-      mbar_init(smem_addr(&p_full[i]), C::kGroup / 32);
-      for (int k = 0; k < 4; ++k) mbar_init(smem_addr(&handed[i][k]), 2);
+      mbar_init(smem_addr(&p_full[i]), C::kSoftmax / 32);
     }
     mbar_init(smem_addr(&pv_done), 1);
     mbar_init(smem_addr(&q_full), C::kSoftmax / 32);
@@ -890,7 +863,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < C::kKeys / 16; ++k) {
           if (k == 6 && more) k_seen = test(k_bar(j + 2), (j + 2) / C::kKStages & 1);
-          umma_f16_tmem_a_if(leader, tmem + C::kOCol, tmem + (j & 1) * 128 + k * 8,
+          umma_f16_tmem_a_if(leader, tmem + C::kOCol,
+                             tmem + (j & 1) * 128 + (k >> 1) * 32 + (k & 1) * 8,
                           umma_sdesc(vb + k * 8192, 2048, 1024), kIdO, (j > 0 || k > 0));
         }
         umma_commit_if(leader, smem_addr(&v_empty[vst]));
@@ -905,114 +879,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
       mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
     }
   } else {
-    // ================================================ softmax: group g takes key tiles g, g + 2, ...
+    // ================================================ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    const int g = warp >> 3, h = (warp >> 2) & 1, quarter = warp & 3;
+    const int cq = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // TMEM lane = row of the tile
-    const uint32_t pair_bar = 1 + g * 4 + quarter;
     const bool rv = real_row(r);
-    const int tok = tile.qbase + (rv ? r / a.group : 0);
-    const int pos = tile.ctx + tok;  // padding rows mirror the tile's first row
+    const int pos = tile.ctx + tile.qbase + (rv ? r / a.group : 0);  // padding rows: the first row's
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t sbuf = tmem + lane_addr + g * 128;
     const uint32_t obuf = tmem + lane_addr + C::kOCol;
 
-    {  // a quarter of the Q row -> shared memory, 128B-swizzled K-major
+    // Q -> shared memory, 128B-swizzled K-major
 #pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
-        const int c = (g * 2 + h) * (D / 32) + cc;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                         q_s + (c >> 3) * (C::kRows * 128) + swz128(r, c & 7)),
-                     "r"(qv[cc].x), "r"(qv[cc].y), "r"(qv[cc].z), "r"(qv[cc].w)
-                     : "memory");
-      }
-      fence_proxy_async();
-      warp_arrive(smem_addr(&q_full));
+    for (int cc = 0; cc < D / 32; ++cc) {
+      const int c = cq * (D / 32) + cc;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       q_s + (c >> 3) * (C::kRows * 128) + swz128(r, c & 7)),
+                   "r"(qv[cc].x), "r"(qv[cc].y), "r"(qv[cc].z), "r"(qv[cc].w)
+                   : "memory");
     }
+    fence_proxy_async();
+    warp_arrive(smem_addr(&q_full));
 
     bool stopped = false;
     float m_run = -INFINITY, l_run = 0.f;  // m in the scores' unit
     const bool prescale = !(a.scale_log2 > 0.f);
     const float mul = prescale ? 1.f : a.scale_log2;
-    auto row_max = [&](int gg) {
-      auto at = [&](int hh) {
-        return __uint_as_float(static_cast<uint32_t>(max_hi[gg][hh][r]) << 16 |
-                               static_cast<uint32_t>(max_lo[gg][hh][r]) << 8);
-      };
-      return fmaxf(at(0), at(1));
-    };
-    for (int j = g; j < ntiles; j += 2) {
-      const bool got = __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&s_full[g]), (j >> 1) & 1,
+    for (int j = 0; j < ntiles; ++j) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&s_full[j & 1]), j >> 1 & 1,
                                                                a.err, a.wait_limit_ns));
-      uint32_t sv[2][32];
-      float mloc = -INFINITY;
-      const int key0 = tile.key_base + j * C::kKeys + h * 64;
-      if (got) {
+      const int key0 = tile.key_base + j * C::kKeys + cq * 32;
+      // O so far, its last product done, goes over to the new base.  P V of tile j - 1 is done when
+      // S(j + 1), issued after it, is; the last tile has its own barrier.
+      auto rebase = [&](float alpha) {
+        if (j == 0) return;
+        const bool more = j + 1 < ntiles;
+        const bool done = __all_sync(
+            0xffffffffu, mbar_wait_short(smem_addr(more ? &s_full[(j + 1) & 1] : &pv_done),
+                                         more ? (j + 1) >> 1 & 1 : 0, a.err, a.wait_limit_ns));
         tmem_fence_after_sync();
-        mloc = load_scores(sbuf + h * 64, sv, prescale, a.scale_log2,
-                           key0 + 63 > tile.ctx + tile.qbase, key0, pos);
-      }
-      // The other group's maxima of tile j - 1; its threads wait for this read, through `handed`,
-      // before they store those of tile j + 1.
-      float before = -INFINITY;
-      if (j > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_short(smem_addr(&handed[g ^ 1][quarter]),
-                                                     ((j - 1) >> 1) & 1, a.err, a.wait_limit_ns)))
-          stopped = true;  // nothing more is written; the pair leaves together below
-        before = row_max(g ^ 1);
-      }
-      const uint32_t up = round_up24(mloc);
-      max_hi[g][h][r] = static_cast<uint16_t>(up >> 16);
-      max_lo[g][h][r] = static_cast<uint8_t>(up >> 8);
-      tmem_fence_before_sync();
-      // both halves have read their scores before either stores P over them
-      if (bar_sync_or(pair_bar, 64, !got || stopped)) {
-        stopped = true;
+        if (done) rescale(obuf + cq * (D / 2), D / 2, alpha);
+        if (!done) softmax_stop = 1;  // no row is written
+      };
+      if (!soften<BF>(tmem + lane_addr + (j & 1) * 128, got, maxima, r, cq, 1 + quarter, prescale,
+                      a.scale_log2, key0 + 31 > tile.ctx + tile.qbase, key0, pos, mul, m_run, l_run,
+                      rebase)) {
+        stopped = true;  // the row's four warps leave together
         break;
       }
-      tmem_fence_after_sync();
-      const float mx = row_max(g);
-      warp_arrive(smem_addr(&handed[g][quarter]));
-      // The base is a function of the maxima so far, so every thread of the row computes the same
-      // one: after tile j - 1 (the other group's), then after tile j.
-      const float m_prev = j > 0 && raises(m_run, before, mul) ? before : m_run;
-      float m_new = m_prev, alpha = 1.f;
-      if (raises(m_prev, mx, mul)) {
-        alpha = ex2_approx((m_prev - mx) * mul);  // 0 when m_prev is -inf
-        m_new = mx;
-      }
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // rare: O so far, its last product done, goes over to the new base.  P V of tile j - 1 is
-        // done when S(j + 1), issued after it, is; the last tile has its own barrier.
-        const bool more = j + 1 < ntiles;
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait_short(smem_addr(more ? &s_full[(j + 1) & 1] : &pv_done),
-                                        more ? (j + 1) >> 1 & 1 : 0, a.err, a.wait_limit_ns)))
-          stopped = true;
-        tmem_fence_after_sync();
-        rescale(obuf + h * D, D, alpha);
-      }
-      // this thread's sum is still against its group's base of two tiles ago
-      if (m_new != m_run) l_run *= ex2_approx((m_run - m_new) * mul);
-      m_run = m_new;
-      l_run += store_weights<BF>(sbuf + h * 32, sv, mul, m_run == -INFINITY ? 0.f : -m_run * mul);
-
       const int tile0 = tile.key_base + j * C::kKeys;
       if (j == ntiles - 1 && tile0 + C::kKeys > tile.key_stop) {
-        // V rows past the last visible key may hold any bits: each thread clears row r of head h
+        // V rows past the last visible key may hold any bits: each thread clears 64 columns of row r
         // once the tile has landed
         const int vst = j % C::kVStages;
         if (!mbar_wait_short(smem_addr(&v_full[vst]), (j / C::kVStages) & 1, a.err,
                              a.wait_limit_ns))
-          stopped = true;
+          softmax_stop = 1;  // no row is written
         else if (tile0 + r >= tile.key_stop)
-          clear_v_row<2>(v_s + vst * C::kVBytes, r, h);
+          clear_v_row<2>(v_s + vst * C::kVBytes, r, cq >> 1, cq & 1);
         fence_proxy_async();
       }
       tmem_wait_st();
       tmem_fence_before_sync();
-      // a warp that gave up hands over nothing; its pair leaves at the next tile's meeting
-      if (!__any_sync(0xffffffffu, stopped)) warp_arrive(smem_addr(&p_full[g]));
+      warp_arrive(smem_addr(&p_full[j & 1]));
     }
     bool ok = !stopped;
     if (ok) ok = mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
@@ -1020,8 +948,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     softmax_sync();
     if (!*reinterpret_cast<volatile int*>(&softmax_stop)) {
       float* red = reinterpret_cast<float*>(smem);  // Q is done once drained
-      red[(g * 2 + h) * C::kRows + r] = l_run;
-      if (h == 0) red[(4 + g) * C::kRows + r] = m_run;
+      red[cq * C::kRows + r] = l_run;
+      if (cq == 0) red[4 * C::kRows + r] = m_run;
     }
   }
   __syncthreads();
@@ -1040,13 +968,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   float inv = 0.f;
   tmem_fence_after_sync();
   if (softmax && ok) {
-    const float m0 = red[4 * C::kRows + r], m1 = ntiles > 1 ? red[5 * C::kRows + r] : -INFINITY;
-    const float m = fmaxf(m0, m1), base = m == -INFINITY ? 0.f : m;
-    const float l = (red[r] + red[C::kRows + r]) * ex2_approx((m0 - base) * mul) +
-                    (red[2 * C::kRows + r] + red[3 * C::kRows + r]) * ex2_approx((m1 - base) * mul);
-    inv = l > 0.f ? 1.f / l : 0.f;
+    const float l = (red[r] + red[C::kRows + r]) + (red[2 * C::kRows + r] + red[3 * C::kRows + r]);
+    inv = l > 0.f ? 1.f / l : 0.f;  // 0: the row sees no key of this range
     if (nsplit > 1 && rv && ch == 0) {
-      a.chunk_m[cell(r)] = m * mul;
+      a.chunk_m[cell(r)] = red[4 * C::kRows + r] * mul;
       a.chunk_l[cell(r)] = l;
     }
   }
