@@ -19,8 +19,7 @@
 //     one score buffer's products while the other buffer is in softmax;
 //   * warps 0 .. 15 are the softmax: all of them take every score buffer in turn, a thread per
 //     (row, quarter of the tile's columns), while the pipe works on the other buffer.  The base m
-//     of a row is raised only when a maximum passes it by more than 2^8 (then O is rescaled in
-//     TMEM).
+//     of a row is raised only when weights against it grow large (then O is rescaled in TMEM).
 // Every wait is bounded; V rows past the last visible key are zeroed before their product.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -41,7 +40,6 @@ struct ChunkCfg {
   static constexpr int kSoftmax = 512, kThreads = kSoftmax + 128;
   static constexpr int kRegsSoftmax = 104, kRegsOther = 64, kLaunchRegs = 96;
   static constexpr uint32_t kTmemCols = 512, kOCol = 256;
-  static constexpr float kRescaleLog2 = 8.f;
   static_assert(kRegsSoftmax * kSoftmax + kRegsOther * 128 <= kLaunchRegs * kThreads,
                 "register split exceeds the launch allocation");
 };
@@ -221,16 +219,9 @@ __device__ __forceinline__ void stream_heads(const DiffArgs& a, const Tile& t,
       mbar_wait_short(smem_addr(&full[j % stages]), (j / stages) & 1, a.err, a.wait_limit_ns);
 }
 
-// A thread's 32 scores from TMEM (scaled where the scale cannot go into the exponent, masked) and
-// their weights 2^(score mul + neg_m), rounded to the element type for the matrix product (at most
-// 2^-11 (fp16) or 2^-8 (bf16) of each weight, at random over the keys), two keys a word.  max: of
-// the scores; returns the unrounded weights' sum.  (Summing the rounded weights instead changes the
-// result's error by under 1%.)
-template <bool BF>
-__device__ __forceinline__ float weigh(uint32_t addr, uint32_t (&pk)[16], float& max, bool prescale,
-                                       float scale_log2, bool masked, int key0, int pos, float mul,
-                                       float neg_m) {
-  uint32_t sv[32];
+// A thread's 32 scores from TMEM, scaled where the scale cannot go into the exponent, masked.
+__device__ __forceinline__ void load_scores(uint32_t addr, uint32_t (&sv)[32], bool prescale,
+                                            float scale_log2, bool masked, int key0, int pos) {
   tmem_ld32(addr, sv);
   tmem_wait_ld();
   tmem_regs_ready(sv);
@@ -243,29 +234,30 @@ __device__ __forceinline__ float weigh(uint32_t addr, uint32_t (&pk)[16], float&
       sv[c] = __float_as_uint(v);
     }
   }
+}
+
+// Their weights 2^(score mul + neg_m), rounded to the element type for the matrix product (at most
+// 2^-11 (fp16) or 2^-8 (bf16) of each weight, at random over the keys), two keys a word; returns
+// the unrounded weights' sum.  (Summing the rounded weights instead changes the result's error by
+// under 1%.)
+template <bool BF>
+__device__ __forceinline__ float weigh(const uint32_t (&sv)[32], uint32_t (&pk)[16], float mul,
+                                       float neg_m) {
   const uint64_t mul2 = f32x2(mul, mul), negm2 = f32x2(neg_m, neg_m);
   uint64_t ps2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-  float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
-    const float v0 = __uint_as_float(sv[k]), v1 = __uint_as_float(sv[k + 1]);
-    m2[(k >> 1) & 1] = fmax3(m2[(k >> 1) & 1], v0, v1);
     float x0, x1;
-    f32x2_split(ffma2(f32x2(v0, v1), mul2, negm2), x0, x1);
+    f32x2_split(ffma2(f32x2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), mul2, negm2), x0,
+                x1);
     const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
     ps2[(k >> 1) & 1] = fadd2(ps2[(k >> 1) & 1], f32x2(p0, p1));
     pk[k >> 1] = pack2<BF>(p0, p1);
   }
-  max = fmaxf(m2[0], m2[1]);
   float s0, s1, s2, s3;
   f32x2_split(ps2[0], s0, s1);
   f32x2_split(ps2[1], s2, s3);
   return (s0 + s1) + (s2 + s3);
-}
-
-// Whether a row's base m gives way to the maximum x (both in the scores' own unit).
-__device__ __forceinline__ bool raises(float m, float x, float mul) {
-  return (x - m) * mul > ChunkCfg::kRescaleLog2 || (m == -INFINITY && x > -INFINITY);
 }
 
 // Columns [0, n) at `addr` of this thread's lane times f.
@@ -308,12 +300,13 @@ struct Maxima {
 };
 
 // One score buffer's softmax by the 512 threads: this thread's row r, columns 32 cq .. + 31 of S at
-// sbuf.  The weights are taken against the row's base m so far; only when a maximum raises it (the
-// first tile, rarely later) are they taken again, from the scores still in TMEM, after `rebase` has
-// brought O to the new base.  So the maxima and their exchange are off the path from S to P; the
-// one meeting of the row's four threads only asks whether anyone raises.  P goes where the
-// thread's own scores were: 16 columns from 32 cq on.  False, for all four of a row's warps, when one
-// of them had no scores (its wait gave up).
+// sbuf.  The weights are taken against the row's base m so far.  Only where that does not do (no
+// base yet, or a thread's 32 weights sum to more than 2^10, so one is above 2^5: they stay far
+// below fp16's 2^16) are the maxima exchanged, O brought to the new base by `rebase` and the
+// weights taken again, from the scores still in TMEM.  So the usual tile computes no maximum, and
+// the one meeting of the row's four threads only asks whether anyone wants a new base.  P goes
+// where the thread's own scores were: 16 columns from 32 cq on.  False, for all four of a row's
+// warps, when one of them had no scores (its wait gave up).
 template <bool BF, typename Rebase>
 __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int r, int cq,
                                        uint32_t meet_bar, bool prescale, float scale_log2,
@@ -322,20 +315,27 @@ __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int 
   uint32_t pk[16];
   float sum = 0.f;
   for (int turn = 0; turn < 2; ++turn) {
+    uint32_t sv[32];
+    if (got) {
+      tmem_fence_after_sync();
+      load_scores(sbuf + 32 * cq, sv, prescale, scale_log2, masked, key0, pos);
+      sum = weigh<BF>(sv, pk, mul, m_run == -INFINITY ? 0.f : -m_run * mul);
+    }
+    if (turn == 1 ||
+        !bar_sync_or(meet_bar, 128, !got || m_run == -INFINITY || !(sum <= 1024.f)))
+      break;
     uint32_t up = 0x7fffff00u;  // NaN: this thread has given up (a maximum itself is never NaN)
     if (got) {
-      float top;
-      tmem_fence_after_sync();
-      sum = weigh<BF>(sbuf + 32 * cq, pk, top, prescale, scale_log2, masked, key0, pos, mul,
-                      m_run == -INFINITY ? 0.f : -m_run * mul);
+      load_scores(sbuf + 32 * cq, sv, prescale, scale_log2, masked, key0, pos);
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(sv[c]));
       up = round_up24(top);
     }
     mx.hi[cq][r] = static_cast<uint16_t>(up >> 16);
     mx.lo[cq][r] = static_cast<uint8_t>(up >> 8);
-    tmem_fence_before_sync();
-    if (!bar_sync_or(meet_bar, 128, !got || raises(m_run, __uint_as_float(up), mul))) break;
-    tmem_fence_after_sync();
-    float top = -INFINITY;
+    bar_sync_or(meet_bar, 128, false);
+    float top = m_run;
     bool lost = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -343,16 +343,15 @@ __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int 
       lost |= hi == 0x7fffu;
       top = fmaxf(top, __uint_as_float(hi << 16 | static_cast<uint32_t>(mx.lo[i][r]) << 8));
     }
+    bar_sync_or(meet_bar, 128, false);  // the maxima are read before a later tile's are stored
     if (__any_sync(0xffffffffu, lost)) return false;
-    float alpha = 1.f;
-    if (raises(m_run, top, mul)) {
-      alpha = ex2_approx((m_run - top) * mul);  // 0 when m_run is still -inf
+    if (__any_sync(0xffffffffu, top != m_run)) {
+      const float alpha = top == m_run ? 1.f : ex2_approx((m_run - top) * mul);
+      rebase(alpha);
+      l_run *= alpha;  // alpha is 0, and l, when m_run is still -inf
       m_run = top;
-      l_run *= alpha;
     }
-    if (__any_sync(0xffffffffu, alpha != 1.f)) rebase(alpha);
   }
-  tmem_fence_after_sync();
   l_run += sum;
   tmem_st16(sbuf + 32 * cq, pk);
   return true;
