@@ -846,6 +846,7 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   a.num_kv_heads = static_cast<int>(hkv);
   a.num_pairs = static_cast<int>(hkv / 2);
   a.group = static_cast<int>(group);
+  a.group_inv = 65536 / a.group + 1;
   a.head_dim = static_cast<int>(d);
   a.block_size = static_cast<int>(k_cache->shape[2]);
   a.max_blocks = static_cast<int>(block_tables->shape[1]);

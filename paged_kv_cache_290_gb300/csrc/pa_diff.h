@@ -17,6 +17,7 @@ struct DiffArgs : AttnArgs {
   float out_scale;
   int part_tokens;       // keys per split-context partition
   int num_pairs;         // num_kv_heads / 2
+  int group_inv;         // 65536 / group + 1
   int stages;            // units in flight per warp of the rows kernel
   int max_seq_len;       // the hint's
   int key_splits;        // ranges of the keys that the chunk kernel's CTAs share out

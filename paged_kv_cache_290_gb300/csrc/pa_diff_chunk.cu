@@ -67,6 +67,15 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// row / group and row % group of a tile row (0 .. 127, group 1 .. 16) by a multiplication: exact
+// there for inv = 65536 / group + 1.
+__device__ __forceinline__ int token_of(const DiffArgs& a, int row) {
+  return (row * a.group_inv) >> 16;
+}
+__device__ __forceinline__ int head_of(const DiffArgs& a, int row) {
+  return row - token_of(a, row) * a.group;
+}
+
 // The chunk tile of a CTA: its rows and keys.
 struct Tile {
   int s, row0, q_len, ctx, qbase, tile_q;
@@ -314,6 +323,8 @@ __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int 
                                        float& l_run, Rebase rebase) {
   uint32_t pk[16];
   float sum = 0.f;
+  // Unrolled, so that the usual tile runs straight through (a 4001-row prompt 111 -> 105 us).
+#pragma unroll 2
   for (int turn = 0; turn < 2; ++turn) {
     uint32_t sv[32];
     if (got) {
@@ -423,6 +434,34 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_wait();
 }
 
+// An arrival on another CTA's mbarrier, and the (bounded) wait for it there.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
+                                                  uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; it < (1u << 28); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 63u) == 63u) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) break;
+    }
+  }
+  atomicOr(err, kErrTimeout);
+  return false;
+}
+
 // The address of `addr` (of this CTA's shared memory) in the CTA of cluster rank `rank`.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
   uint32_t r;
@@ -454,38 +493,7 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
 
   const int pair = blockIdx.y, nsplit = a.key_splits;
   const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
-  Tile tile;
-  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), gridDim.x - 1 - blockIdx.x, z, split,
-                     blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
-                     blockIdx.x == 0 && split == 0, tile))
-    return;
-  // the cell of a row's partial, when the keys are split
-  auto cell = [&](int row, int map) {
-    return (static_cast<int64_t>(tile.row0 + tile.qbase + row / a.group) * a.num_q_heads +
-            2 * (pair * a.group + row % a.group) + map) * nsplit + split;
-  };
-  auto real_row = [&](int row) {
-    return row < tile.tile_q * a.group && tile.qbase + row / a.group < tile.q_len;
-  };
-  // A range without a result says so (l = -1), and the merge leaves such rows alone.
-  auto no_result = [&](int row, int map) {
-    if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row, map)] = -1.f;
-  };
-  // This thread's share of Q (a quarter of each map's row), in flight while the barriers are set up.
-  uint4 qv[2][D / 32];
-  if (warp < C::kSoftmax / 32) {
-    const int r = (warp & 3) * 32 + lane;
-    const bool rv = real_row(r);
-    const __half* qrow =
-        a.q + static_cast<int64_t>(tile.row0 + tile.qbase + (rv ? r / a.group : 0)) * a.q_stride +
-        static_cast<int64_t>(2 * (pair * a.group + r % a.group)) * D + (warp >> 2) * (D / 4);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        qv[t][c] = rv ? __ldg(reinterpret_cast<const uint4*>(qrow + t * D) + c)
-                      : make_uint4(0u, 0u, 0u, 0u);
-  }
+  // Barriers and TMEM are set up while the search for the tile waits for its loads.
   if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < C::kKStages; ++i) {
@@ -506,8 +514,41 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     softmax_stop = 0;
   }
   tmem_fence_before_sync();
-  __syncthreads();
+  Tile tile;
+  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), gridDim.x - 1 - blockIdx.x, z, split,
+                     blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
+                     blockIdx.x == 0 && split == 0, tile)) {
+    if (warp == 0) free_tmem(tmem_base, C::kTmemCols);
+    return;
+  }
   tmem_fence_after_sync();
+  // the cell of a row's partial, when the keys are split
+  auto cell = [&](int row, int map) {
+    return (static_cast<int64_t>(tile.row0 + tile.qbase + token_of(a, row)) * a.num_q_heads +
+            2 * (pair * a.group + head_of(a, row)) + map) * nsplit + split;
+  };
+  auto real_row = [&](int row) {
+    return row < tile.tile_q * a.group && tile.qbase + token_of(a, row) < tile.q_len;
+  };
+  // A range without a result says so (l = -1), and the merge leaves such rows alone.
+  auto no_result = [&](int row, int map) {
+    if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row, map)] = -1.f;
+  };
+  // This thread's share of Q: a quarter of each map's row.
+  uint4 qv[2][D / 32];
+  if (warp < C::kSoftmax / 32) {
+    const int r = (warp & 3) * 32 + lane;
+    const bool rv = real_row(r);
+    const __half* qrow =
+        a.q + static_cast<int64_t>(tile.row0 + tile.qbase + (rv ? token_of(a, r) : 0)) * a.q_stride +
+        static_cast<int64_t>(2 * (pair * a.group + head_of(a, r))) * D + (warp >> 2) * (D / 4);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+        qv[t][c] = rv ? __ldg(reinterpret_cast<const uint4*>(qrow + t * D) + c)
+                      : make_uint4(0u, 0u, 0u, 0u);
+  }
   const uint32_t tmem = tmem_base;
   const int ntiles = tile.ntiles;
 
@@ -597,8 +638,8 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     const int cq = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // TMEM lane = row of the tile
     const bool rv = real_row(r);
-    const int tok = tile.qbase + (rv ? r / a.group : 0);
-    const int head = pair * a.group + r % a.group;
+    const int tok = tile.qbase + (rv ? token_of(a, r) : 0);
+    const int head = pair * a.group + head_of(a, r);
     const int pos = tile.ctx + tok;  // padding rows mirror the tile's first row
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t obuf = tmem + lane_addr + C::kOCol;
@@ -654,6 +695,8 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
     }
 
     // ---- the row's sums of both maps; every softmax thread meets here
+    const int64_t row = tile.row0 + tok;
+    const float lam = __ldg(a.lam + row * a.lam_stride + head);  // used after the waits below
     bool ok = !stopped;
     if (ok) ok = mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
     float* red = reinterpret_cast<float*>(smem);  // Q and the rings are done once drained
@@ -697,8 +740,6 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
           }
         }
       } else {
-        const int64_t row = tile.row0 + tok;
-        const float lam = __ldg(a.lam + row * a.lam_stride + head);
         float y[kCols], ss = 0.f;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
@@ -735,7 +776,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   __shared__ __align__(8) uint64_t v_full[C::kVStages], v_empty[C::kVStages];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done, q_full, drain;
   __shared__ uint32_t tmem_base;
-  __shared__ __align__(8) uint64_t rows_in;  // the other map's rows have arrived
+  // the other CTA's rings may be written; the other map's rows have arrived
+  __shared__ __align__(8) uint64_t peer_free, rows_in;
   __shared__ TileScan scan;
   __shared__ int softmax_stop;
   __shared__ Maxima maxima;
@@ -749,34 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
 
   const int map = blockIdx.x & 1, pair = blockIdx.y, nsplit = a.key_splits;  // map = cluster rank
   const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
-  Tile tile;
-  // both CTAs of the cluster see the same tile: they leave early together or not at all
-  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), (gridDim.x - 1 - blockIdx.x) / 2, z, split,
-                     blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
-                     blockIdx.x == 0 && split == 0, tile))
-    return;
-  auto cell = [&](int row) {
-    return (static_cast<int64_t>(tile.row0 + tile.qbase + row / a.group) * a.num_q_heads +
-            2 * (pair * a.group + row % a.group) + map) * nsplit + split;
-  };
-  auto real_row = [&](int row) {
-    return row < tile.tile_q * a.group && tile.qbase + row / a.group < tile.q_len;
-  };
-  auto no_result = [&](int row) {
-    if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row)] = -1.f;
-  };
-  // This thread's share of Q (a quarter of a row), in flight while the barriers are set up.
-  uint4 qv[D / 32];
-  if (warp < C::kSoftmax / 32) {
-    const int r = (warp & 3) * 32 + lane;
-    const bool rv = real_row(r);
-    const __half* qrow =
-        a.q + static_cast<int64_t>(tile.row0 + tile.qbase + (rv ? r / a.group : 0)) * a.q_stride +
-        static_cast<int64_t>(2 * (pair * a.group + r % a.group) + map) * D + (warp >> 2) * (D / 4);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-      qv[c] = rv ? __ldg(reinterpret_cast<const uint4*>(qrow) + c) : make_uint4(0u, 0u, 0u, 0u);
-  }
+  // Barriers and TMEM are set up while the search for the tile waits for its loads.
   if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < C::kKStages; ++i) {
@@ -795,13 +810,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     mbar_init(smem_addr(&q_full), C::kSoftmax / 32);
     mbar_init(smem_addr(&drain), 1);
     mbar_init(smem_addr(&rows_in), 1);
+    mbar_init(smem_addr(&peer_free), 1);
     mbar_init_fence();
     softmax_stop = 0;
-    mbar_arrive_expect_tx(smem_addr(&rows_in), 64 * 2 * D * 4);
   }
   tmem_fence_before_sync();
-  __syncthreads();
+  Tile tile;
+  // both CTAs of the cluster see the same tile: they leave early together or not at all
+  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), (gridDim.x - 1 - blockIdx.x) / 2, z, split,
+                     blockIdx.x == 0 && pair == 0 && blockIdx.z == 0,
+                     blockIdx.x == 0 && split == 0, tile)) {
+    if (warp == 0) free_tmem(tmem_base, C::kTmemCols);
+    return;
+  }
   tmem_fence_after_sync();
+  cluster_arrive();  // this CTA's barriers are set up
+  auto cell = [&](int row) {
+    return (static_cast<int64_t>(tile.row0 + tile.qbase + token_of(a, row)) * a.num_q_heads +
+            2 * (pair * a.group + head_of(a, row)) + map) * nsplit + split;
+  };
+  auto real_row = [&](int row) {
+    return row < tile.tile_q * a.group && tile.qbase + token_of(a, row) < tile.q_len;
+  };
+  auto no_result = [&](int row) {
+    if (nsplit > 1 && real_row(row)) a.chunk_l[cell(row)] = -1.f;
+  };
+  // This thread's share of Q: a quarter of a row.
+  uint4 qv[D / 32];
+  if (warp < C::kSoftmax / 32) {
+    const int r = (warp & 3) * 32 + lane;
+    const bool rv = real_row(r);
+    const __half* qrow =
+        a.q + static_cast<int64_t>(tile.row0 + tile.qbase + (rv ? token_of(a, r) : 0)) * a.q_stride +
+        static_cast<int64_t>(2 * (pair * a.group + head_of(a, r)) + map) * D + (warp >> 2) * (D / 4);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      qv[c] = rv ? __ldg(reinterpret_cast<const uint4*>(qrow) + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
   const uint32_t tmem = tmem_base;
   const int ntiles = tile.ntiles;
 
@@ -883,7 +928,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     const int cq = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // TMEM lane = row of the tile
     const bool rv = real_row(r);
-    const int pos = tile.ctx + tile.qbase + (rv ? r / a.group : 0);  // padding rows: the first row's
+    const int pos = tile.ctx + tile.qbase + (rv ? token_of(a, r) : 0);  // padding rows: the first row's
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t obuf = tmem + lane_addr + C::kOCol;
 
@@ -941,6 +986,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
       tmem_fence_before_sync();
       warp_arrive(smem_addr(&p_full[j & 1]));
     }
+    // The norm weights go where Q was (every S is done), for the rows that this CTA finishes.
+    if (a.norm_w && tid < 2 * D / 4)
+      reinterpret_cast<float4*>(smem + 8192)[tid] =
+          __ldg(reinterpret_cast<const float4*>(a.norm_w) + tid);
     bool ok = !stopped;
     if (ok) ok = mbar_wait_short(smem_addr(&drain), 0, a.err, a.wait_limit_ns);
     if (!ok) softmax_stop = 1;
@@ -952,6 +1001,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     }
   }
   __syncthreads();
+  cluster_wait();  // so are the other CTA's
 
   // ---- the row's sum; then rows change sides: CTA `map` finishes rows 64 map .. 64 map + 63
   const int ch = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;  // softmax warps
@@ -994,7 +1044,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     // Normalised sums -> shared memory, [row of the half][64 chunks of 16 bytes], a chunk's place
     // XORed with the row (conflict-free both ways): the rows this CTA finishes where K was, the
     // others in V's second stage, from which one bulk copy takes them to the other CTA's first.
-    cluster_arrive();  // this CTA's tiles are done with
+    // This CTA's rings are done with: the other one may send.
+    if (tid == 0) {
+      mbar_arrive_expect_tx(smem_addr(&rows_in), 64 * 2 * D * 4);
+      mbar_arrive_cluster(cluster_addr(smem_addr(&peer_free), map ^ 1));
+    }
     const uint32_t own_s = k_s, out_s = v_s + C::kVBytes, in_s = v_s;
     // column of y of chunk 8 i + sub: O's 64-column pieces are in V's order (half, head)
     auto out_column = [](int i, int sub) {
@@ -1004,6 +1058,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
     auto chunk_at = [&](uint32_t base, int row, int c) {
       return base + row * (2 * D * 4) + ((c ^ (row & 7)) << 4);
     };
+    // eight threads per row, 32 columns each (every eighth chunk)
+    const int row = tid >> 3, sub = tid & 7, rr = 64 * map + row;
+    const bool real = softmax && real_row(rr);
+    const int64_t token = tile.row0 + tile.qbase + (real ? token_of(a, rr) : 0);
+    const int dhead = pair * a.group + (real ? head_of(a, rr) : 0);
+    const float lam = real ? __ldg(a.lam + token * a.lam_stride + dhead) : 0.f;
     if (softmax && ok) {
 #pragma unroll
       for (int c0 = 0; c0 < kCols; c0 += 32) {
@@ -1019,22 +1079,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
                        "f"(__uint_as_float(t[c + 2]) * inv), "f"(__uint_as_float(t[c + 3]) * inv)
                        : "memory");
       }
-      fence_proxy_async();  // the bulk copy reads what these threads wrote
+      if (!mine) {
+        // the 32 rows of this quarter go over as soon as its four warps have stored them
+        fence_proxy_async();  // the bulk copy reads what these threads wrote
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter) : "memory");
+        const uint32_t at = (quarter & 1) * (32 * 2 * D * 4);
+        if (ch == 0 && lane == 0 &&
+            mbar_wait_cluster(smem_addr(&peer_free), 0, a.err, a.wait_limit_ns))
+          asm volatile(
+              "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], "
+              "%2, [%3];" ::"r"(cluster_addr(in_s + at, map ^ 1)),
+              "r"(out_s + at), "r"(32 * 2 * D * 4),
+              "r"(cluster_addr(smem_addr(&rows_in), map ^ 1))
+              : "memory");
+      }
+      softmax_sync();  // this CTA's own rows are stored
     }
-    __syncthreads();
-    // eight threads per row, 32 columns each (every eighth chunk)
-    const int row = tid >> 3, sub = tid & 7, rr = 64 * map + row;
-    const bool real = softmax && real_row(rr);
-    const int64_t token = tile.row0 + tile.qbase + (real ? rr / a.group : 0);
-    const int dhead = pair * a.group + rr % a.group;
-    const float lam = real ? __ldg(a.lam + token * a.lam_stride + dhead) : 0.f;
-    cluster_wait();  // so are the other CTA's
-    if (tid == 0 && ok)
-      asm volatile(
-          "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-          "[%3];" ::"r"(cluster_addr(in_s, map ^ 1)),
-          "r"(out_s), "r"(64 * 2 * D * 4), "r"(cluster_addr(smem_addr(&rows_in), map ^ 1))
-          : "memory");
     // A CTA that failed sends nothing: the other one's wait runs out and its rows stay unwritten.
     if (softmax && ok && __all_sync(0xffffffffu, mbar_wait_short(smem_addr(&rows_in), 0, a.err,
                                                                  a.wait_limit_ns))) {
@@ -1072,7 +1132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (a.norm_w) {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(a.norm_w + out_column(i, sub)));
+          const float4 w = reinterpret_cast<const float4*>(smem + 8192)[out_column(i, sub) / 4];
           y[4 * i] *= w.x;
           y[4 * i + 1] *= w.y;
           y[4 * i + 2] *= w.z;
