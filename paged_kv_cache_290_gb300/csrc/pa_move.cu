@@ -3,16 +3,19 @@
 //
 // Plan (host, once per list of moves).  Moves are put in chain order, each chain from its end:
 // the move out of a page then comes before the move into it.  Consecutive moves form groups of
-// kGroup, and groups form launches of at most kMaxMoves moves.  A thread owns one 16-byte chunk
-// of every page of a group: it loads the chunk of all the group's sources, then stores them to
-// the destinations, so inside a group any chain or cycle is safe.  Launches run one after the
-// other.  What is left is a page that another group overwrites in the same launch, or that an
-// earlier launch has overwritten: those sources (one or two per kGroup moves of a long chain,
-// none where holes are filled) are first copied into the workspace and read from there.
+// kGroup, and groups form launches of at most kMaxMoves moves.  A CTA (one warp) owns the same
+// slice of every page of a group: it copies the slices of all the group's sources into shared
+// memory (bulk copies), waits for them, then copies them to the destinations, so inside a group
+// any chain or cycle is safe.  Launches run one after the other.  What is left is a page that
+// another group overwrites in the same launch, or that an earlier launch has overwritten: those
+// sources (one or two per kGroup moves of a long chain, none where holes are filled) are first
+// copied into the workspace and read from there.
 //
-// Bound by HBM: each moved byte is read and written once, plus staging (at most about 2 in
-// kGroup of the moves).  The moves travel as kernel arguments: no upload, and a captured launch
-// keeps its own copy.
+// Bound by HBM: each moved byte is read and written once, plus staging (about 1 in kGroup of a
+// chain's moves, read and written once more).  4096 pages of 8 layers put in order (2.1 GB, long
+// cycles) 666 us = 6.4 TB/s of moved bytes read and written, 0.96 of the measured copy rate (groups of 8 in
+// registers, a thread per 16 bytes: 729 us, an eighth of the pages staged; 16 x 2 KB 680 us).  The
+// moves travel as kernel arguments: no upload, and a captured launch keeps its own copy.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -28,11 +31,15 @@
 namespace pa {
 namespace {
 
-constexpr int kGroup = 8;
+constexpr int kGroup = 32;
 // Moves per launch, which travel as kernel arguments: 12 KB of the 32 KB there are.  A short list
 // takes the small size, whose arguments stay below 4 KB (a launch of the small size costs 3.0 us on the host).
 constexpr int kMaxMoves = 1024, kFewMoves = 256;
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the renaming
+// Moves and bytes of a page per CTA: a list with chains keeps the plan's groups together; one
+// without takes smaller groups of longer slices, which start sooner (48 moves 5.8 -> 4.4 us, 1501
+// holes of an FP8 pool 67 -> 64.5 us).
+constexpr int kLooseGroup = 8, kSlice = 1024, kLooseSlice = 2048;
 static_assert(kMaxMoves % kGroup == 0 && kFewMoves % kGroup == 0, "a group lies in one launch");
 
 template <int N>
@@ -42,7 +49,9 @@ struct MoveArgs {
   uint4* stage;          // [slot][layer of the batch][K, V][chunks]
   int64_t layer_stride;  // chunks between layers of the pools
   int64_t chunks;        // 16-byte chunks of one page of K (or V)
+  unsigned* err;
   int layer0, layers;    // the batch of layers this launch covers
+  int group, slice;      // moves, and bytes of a page, of a CTA
   int n;
   int32_t* old_ids;      // tables: the move's old and new id by position, and a page's position
   int32_t* new_ids;
@@ -53,34 +62,52 @@ struct MoveArgs {
   int32_t id[N];   // the moved page's old id
 };
 
-__device__ __forceinline__ uint4 load_once(const uint4* p) { return __ldcs(p); }
-__device__ __forceinline__ void store_once(uint4* p, const uint4& x) { __stcs(p, x); }
-
 template <int N>
-__global__ void __launch_bounds__(kThreads) move_kernel(const __grid_constant__ MoveArgs<N> a) {
-  const int g0 = static_cast<int>(blockIdx.y) * kGroup;
+__global__ void __launch_bounds__(32) move_kernel(const __grid_constant__ MoveArgs<N> a) {
+  extern __shared__ __align__(128) uint8_t buf[];  // [move of the group][slice]
+  __shared__ __align__(8) uint64_t full;
+  const int g0 = static_cast<int>(blockIdx.y) * a.group, n = min(a.group, a.n - g0);
   const int lz = static_cast<int>(blockIdx.z) >> 1, kv = static_cast<int>(blockIdx.z) & 1;
-  if (a.position && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x < kGroup) {
-    const int i = g0 + static_cast<int>(threadIdx.x);
-    if (i < a.n) {
-      a.old_ids[a.base + i] = a.id[i];
-      a.new_ids[a.base + i] = a.dst[i];
-      a.position[a.id[i]] = a.base + i;
+  const int lane = threadIdx.x;
+  if (a.position && blockIdx.x == 0 && blockIdx.z == 0)
+    for (int i = lane; i < n; i += 32) {
+      a.old_ids[a.base + g0 + i] = a.id[g0 + i];
+      a.new_ids[a.base + g0 + i] = a.dst[g0 + i];
+      a.position[a.id[g0 + i]] = a.base + g0 + i;
     }
-  }
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (c >= a.chunks) return;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * (a.slice / 16);
+  const int bytes = static_cast<int>(min(static_cast<int64_t>(a.slice), (a.chunks - c) * 16));
   uint4* pool = (kv ? a.v : a.k) + (a.layer0 + lz) * a.layer_stride + c;
   uint4* stage = a.stage + (static_cast<int64_t>(lz) * 2 + kv) * a.chunks + c;
   const int64_t slot = static_cast<int64_t>(a.layers) * 2 * a.chunks;  // chunks per slot
   auto at = [&](int32_t i) { return i >= 0 ? pool + i * a.chunks : stage + ~i * slot; };
-  uint4 x[kGroup];
-#pragma unroll
-  for (int i = 0; i < kGroup; ++i)
-    if (g0 + i < a.n) x[i] = load_once(at(a.src[g0 + i]));
-#pragma unroll
-  for (int i = 0; i < kGroup; ++i)
-    if (g0 + i < a.n) store_once(at(a.dst[g0 + i]), x[i]);
+  const uint32_t bar = smem_addr(&full), base = smem_addr(buf);
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    mbar_init_fence();
+    mbar_arrive_expect_tx(bar, n * bytes);
+  }
+  __syncwarp();
+  for (int i = lane; i < n; i += 32)
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(base + i * a.slice),
+        "l"(at(a.src[g0 + i])), "r"(bytes), "r"(bar)
+        : "memory");
+  // A copy that never lands (no legitimate wait takes two seconds) leaves the destinations alone,
+  // and is given as long again before the CTA retires.
+  if (!__all_sync(0xffffffffu, mbar_wait_short(bar, 0, a.err))) {
+    mbar_wait_short(bar, 0, a.err);
+    return;
+  }
+  __syncwarp();
+  for (int i = lane; i < n; i += 32)
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                     at(a.dst[g0 + i])),
+                 "r"(base + i * a.slice), "r"(bytes)
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // A moved page's id is replaced.  `position` is meaningful for moved pages only: any other entry
@@ -106,6 +133,7 @@ struct pa_move_plan {
   int64_t num_blocks = 0;
   std::vector<int32_t> src, dst, id;  // the moves in order; src: page, or ~slot
   std::vector<int32_t> staged;        // page of each workspace slot
+  bool chained = false;               // some page is both left and entered
 };
 
 namespace {
@@ -133,7 +161,9 @@ void make_plan(pa_move_plan* p, const int32_t* pairs, int64_t n) {
   p->src = p->id;
   for (size_t j = 0; j < p->src.size(); ++j) {
     const int32_t i = order[p->id[j]];  // the move that overwrites this source
-    if (i < 0 || static_cast<size_t>(i) / pa::kGroup == j / pa::kGroup) continue;
+    if (i < 0) continue;
+    p->chained = true;
+    if (static_cast<size_t>(i) / pa::kGroup == j / pa::kGroup) continue;
     if (static_cast<size_t>(i) > j && static_cast<size_t>(i) / pa::kMaxMoves != j / pa::kMaxMoves)
       continue;  // a later launch
     p->src[j] = ~static_cast<int32_t>(p->staged.size());
@@ -287,6 +317,8 @@ int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_
       tables ? reinterpret_cast<int32_t*>(ws + 2 * up256(n * sizeof(int32_t))) : nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
+  unsigned* err = nullptr;
+  if ((e = error_word(stream, &err)) != cudaSuccess) return cuda_fail(e, "error word");
   auto run = [&](auto& a, int most) -> int {
     a.k = static_cast<uint4*>(kl.data);
     a.v = static_cast<uint4*>(vl.data);
@@ -295,11 +327,14 @@ int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_
     a.chunks = page / per16;
     a.old_ids = old_ids;
     a.new_ids = new_ids;
+    a.err = err;
+    a.group = plan->chained ? kGroup : kLooseGroup;
+    a.slice = plan->chained ? kSlice : kLooseSlice;
     auto launch = [&]() {
-      const dim3 grid(static_cast<unsigned>((a.chunks + kThreads - 1) / kThreads),
-                      static_cast<unsigned>((a.n + kGroup - 1) / kGroup),
+      const dim3 grid(static_cast<unsigned>((a.chunks * 16 + a.slice - 1) / a.slice),
+                      static_cast<unsigned>((a.n + a.group - 1) / a.group),
                       static_cast<unsigned>(2 * a.layers));
-      move_kernel<<<grid, kThreads, 0, st>>>(a);
+      move_kernel<<<grid, 32, a.group * a.slice, st>>>(a);  // 16 or 32 KB of shared memory
       return cudaGetLastError();
     };
     for (int64_t l0 = 0; l0 < layers; l0 += batch) {
