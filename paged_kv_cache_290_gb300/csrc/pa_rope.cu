@@ -17,7 +17,8 @@
 // 16-byte loads and stores each, one task's loads in flight while another's is turned.  Four
 // CTAs an SM (64 registers): 8192 tokens of 64 + 8 heads of 128, bf16, 60 us = 5.6 TB/s, 0.84 of
 // the measured copy rate (with 1 / 4 / 8 tokens a CTA 67 / 62 / 66 us; five CTAs of 48
-// registers 76; 128, 384 or 512 threads 60 to 76).  K/V go to scattered slots, 256 bytes each.
+// registers 76; 128, 384 or 512 threads 60 to 76); into an E4M3 pool three CTAs of 80 (8192 tokens
+// of 32 + 8 heads 50 us; two CTAs 62).  K/V go to scattered slots, 256 bytes each.
 // A decode step of 64 tokens (32 + 8 heads): 2.8 us on the device.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -130,7 +131,7 @@ __device__ __forceinline__ void rotate8(float (&x)[8], float (&y)[8], const floa
 // tokens blockIdx.x * kTokens .. and heads blockIdx.y, blockIdx.y + gridDim.y, ... in units of
 // kSlots heads; heads 0 .. hq-1 are q's, then k's, then v's.
 template <int D, bool BF, bool F8, int kTokens>
-__global__ void __launch_bounds__(kThreads, F8 ? 2 : 4) rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, F8 ? 3 : 4) rope_and_cache_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kCols = D / 16, kSlots = kThreads / kCols;
   __shared__ __align__(16) float cos_s[kTokens][kMaxPairs], sin_s[kTokens][kMaxPairs];
   grid_launch_dependents();
@@ -262,7 +263,7 @@ cudaError_t launch(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (a.num_tokens >= 8 * num_sms) {
+  if (a.num_tokens >= 4 * num_sms) {
     cfg.gridDim = dim3(static_cast<unsigned>((a.num_tokens + 1) / 2));
     return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<D, BF, F8, 2>, a);
   }
