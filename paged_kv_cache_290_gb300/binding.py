@@ -47,8 +47,7 @@ EXPORTED = ("pa_reshape_and_cache", "pa_attention_workspace_size", "pa_attention
 
 # Byte tensors are E4M3 codes (the only one-byte type of the ABI).
 _DTYPES = {torch.float16: PA_F16, torch.int32: PA_I32, torch.int64: PA_I64,
-           torch.uint8: PA_F8E4M3, torch.float8_e4m3fn: PA_F8E4M3, torch.bfloat16: PA_BF16,
-           torch.float32: PA_F32}
+           torch.uint8: PA_F8E4M3, torch.float8_e4m3fn: PA_F8E4M3, torch.bfloat16: PA_BF16}
 
 
 class PATensor(ctypes.Structure):

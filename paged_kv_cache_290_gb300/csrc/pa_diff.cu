@@ -30,9 +30,8 @@
 #include <string>
 
 #include "pa.h"
-#include "pa_chunk.cuh"
 #include "pa_common.cuh"
-#include "pa_diff.h"
+#include "pa_diff.cuh"
 #include "pa_host.h"
 
 namespace pa {
@@ -131,7 +130,11 @@ __global__ void __launch_bounds__(RowsCfg<D, NT>::kThreads)
                       : 0;
   }
   const int q_len = row_end - row0;
-  if (q_len < 1 || q_len > a.verify_rows) return leave();
+  if (q_len < 1 || q_len > a.verify_rows) {
+    // Longer than the hint's max_query_len: nobody's, unless chunk kernels were launched.
+    if (q_len > 1 && a.prefill_seqs == 0 && lead && j == 0 && tid == 0) atomicOr(a.err, kErrHint);
+    return leave();
+  }
   if (row0 < 0 || row0 + q_len > a.num_tokens || L < q_len || (L + BS - 1) / BS > a.max_blocks) {
     if (lead && tid == 0) atomicOr(a.err, kErrDescriptor);
     return leave();
@@ -556,16 +559,16 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffArgs a) {
   join_maps<D, BF>(a, any, a.part_o, a.part_m, a.part_l, c, nparts, row0 + qi, head);
 }
 
-// The same for the chunk kernel's partials: grid y = rank of the chunk's sequence, x over its
-// (row, head)s.
+// The same for the chunk kernel's partials: grid y = rank of the chunk's sequence, as in the chunk
+// kernel, x over its (row, head)s.
 template <int D, bool BF>
 __global__ void __launch_bounds__(128) diff_chunk_merge_kernel(const DiffArgs a) {
-  __shared__ int warp_count[4], chosen_seq;
-  const int s = find_prefill_seq<128>(a, warp_count, &chosen_seq, blockIdx.y, false);
-  if (s < 0) return;
+  __shared__ ChunkScan<128> scan;
+  __shared__ int keys[128];
+  find_chunk(a, scan, keys, blockIdx.y, false);
+  if (scan.s < 0) return;
   const int map = (threadIdx.x >> 5) & 1, heads = a.num_q_heads / 2;
-  const int row0 = a.query_start_loc[s], q_len = a.query_start_loc[s + 1] - row0;
-  const int L = a.seq_lens[s];
+  const int row0 = scan.row0, q_len = scan.q_len, L = scan.L;
   if (q_len > L || (L + a.block_size - 1) / a.block_size > a.max_blocks || row0 < 0 ||
       row0 + q_len > a.num_tokens || q_len > a.max_query_len || L > a.max_seq_len)
     return;
@@ -680,8 +683,14 @@ DiffPlan diff_plan(int64_t t, int64_t n, int64_t hq, int64_t hkv, int64_t d,
                    const pa_batch_hint& hint) {
   DiffPlan p{};
   const int64_t group = hq / hkv;
-  // Verify rows: up to 8 columns (one column group) of the rows kernel, which reads the keys once
-  const bool verify = hint.max_query_len * group <= 8;
+  // Short chunks (speculative verify, ends of prompts) go to the rows kernel too: always up to 8
+  // columns (one group, which reads the keys once), and beyond while its grid of 256-key partitions
+  // is small.  The chunk kernel takes 12 to 16 us for the smallest chunk.  One chunk of 16 rows
+  // behind 1000 keys (32 + 8 heads of 128): rows 12.4, chunk 18.2 us; 32 rows 21.0 / 25.6; 64 rows
+  // 34.2 / 25.6; heads of 64: 32 rows 13.9 / 25.0, 64 rows 21.2 / 25.2, 128 rows 25.8 / 25.8.
+  const int64_t columns = hint.max_query_len * group;
+  const int64_t units = n * (hkv / 2) * ((columns + 7) / 8) * ((hint.max_seq_len + int64_t{255}) / 256);
+  const bool verify = columns <= 8 || units <= (d == 64 ? 4 : 2) * kSms;
   p.chunks = hint.max_query_len > 1 && !verify;
   p.rows = !(p.chunks && hint.num_prefill_seqs >= n);
   p.rows_per_seq = p.chunks ? 1 : hint.max_query_len;
@@ -692,8 +701,8 @@ DiffPlan diff_plan(int64_t t, int64_t n, int64_t hq, int64_t hkv, int64_t d,
   // 32 + 8 heads of 128 in us, with partitions of 128 / 256 / 512 / 1024: 1 sequence of 4096 keys
   // 10.5 / 11.3 / 15.2 / 24.8; 4 of them 22.1 / 16.6 / 18.0 / 25.8; 8: 32.3 / 31.4 / 25.8 / 27.9;
   // 16: 52.1 / 49.4 / 51.1 / 45.8; 64 of 512 .. 4096 keys 107 / 96.5 / 94.6 / 97.2.
-  const int64_t columns = p.rows_per_seq * group, per_cta = columns <= 4 ? 4 : 8;
-  const int64_t row_ctas = n * (hkv / 2) * ((columns + per_cta - 1) / per_cta);
+  const int64_t row_cols = p.rows_per_seq * group, per_cta = row_cols <= 4 ? 4 : 8;
+  const int64_t row_ctas = n * (hkv / 2) * ((row_cols + per_cta - 1) / per_cta);
   auto parts_of = [&](int64_t tokens) { return (hint.max_seq_len + tokens - 1) / tokens; };
   p.part_tokens = 128;
   while (p.part_tokens < 1024 && row_ctas * parts_of(p.part_tokens) > 2 * kSms)
@@ -856,7 +865,7 @@ int pa_diff_attention(const pa_tensor* q, const pa_tensor* k_cache, const pa_ten
   a.max_query_len = hint->max_query_len;
   a.max_seq_len = hint->max_seq_len;
   a.verify_rows = plan.rows_per_seq;
-  a.prefill_seqs = plan.prefill_seqs;
+  a.prefill_seqs = plan.chunks ? plan.prefill_seqs : 0;
   a.decode_skipped = plan.rows ? 0 : 1;
   a.key_splits = plan.key_splits;
   a.scale_log2 = scale * 1.4426950408889634f;

@@ -27,7 +27,7 @@
 #include <algorithm>
 
 #include "pa_common.cuh"
-#include "pa_diff.h"
+#include "pa_diff.cuh"
 #include "pa_host.h"
 
 namespace pa {
@@ -49,7 +49,7 @@ struct BothCfg : ChunkCfg {                       // d = 64
   static constexpr int kStageBytes = 2 * kTileBytes;  // K1 and K2, or the two halves of V
   static constexpr int kKStages = 2, kVStages = 3;
   static constexpr int kSmemBytes = 2 * kTileBytes + (kKStages + kVStages) * kStageBytes + 1024;
-  static_assert(kSmemBytes + 3072 <= 232448, "dynamic + static shared memory fit one SM");
+  static_assert(kSmemBytes + 4096 <= 232448, "dynamic + static shared memory fit one SM");
 };
 
 struct MapCfg : ChunkCfg {                        // d = 128
@@ -85,58 +85,14 @@ struct Tile {
 };
 
 // Finds and checks the tile; false when the CTA has none (errors are reported).  All threads of
-// the block call it.  Grid row z serves the sequence of rank z among those with more than one
-// query row: longest first while the batch has at most 128 sequences (the longest CTAs then start
-// first and the grid's tail is short: 4 x 512 rows behind 2k to 7.5k keys 206 against 215 us in batch order), else in batch
-// order.  Every thread holds one sequence's descriptor, and the chosen one is handed on through
-// shared memory, without a second round of loads.  keys: 128 words that nothing uses yet (of Q's
-// tile, which only generic stores fill).
-struct TileScan {
-  int warp_count[ChunkCfg::kThreads / 32];
-  int s, row0, q_len, L;
-};
+// the block call it.  keys: 128 words that nothing uses yet (of Q's tile, which only generic
+// stores fill).
 template <int BS>
-__device__ __forceinline__ bool find_tile(const DiffArgs& a, TileScan& sc, int* keys, int qt, int z, int split,
-                                          bool first, bool lead, Tile& t) {
-  constexpr int kThreads = ChunkCfg::kThreads;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) sc.s = -1;
-  int found = 0;
-  const bool sorted = a.num_seqs <= 128;
-  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
-    const int si = s0 + tid;
-    const bool in = si < a.num_seqs;
-    const int row0 = in ? a.query_start_loc[si] : 0;
-    const int q_len = in ? a.query_start_loc[si + 1] - row0 : 0;
-    const int L = in ? a.seq_lens[si] : 0;
-    const unsigned bal = __ballot_sync(0xffffffffu, q_len > 1);
-    if (a.decode_skipped && first && __any_sync(0xffffffffu, q_len == 1) && lane == 0)
-      atomicOr(a.err, kErrHint);
-    if (lane == 0) sc.warp_count[warp] = __popc(bal);
-    const int key = q_len > 1 ? max(L, 0) : -1;
-    if (sorted && tid < 128) keys[tid] = key;
-    __syncthreads();
-    int rank = found + __popc(bal & ((1u << lane) - 1u));
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      rank += w < warp ? sc.warp_count[w] : 0;
-      found += sc.warp_count[w];
-    }
-    if (sorted && q_len > 1) {
-      rank = 0;
-      for (int j = 0; j < a.num_seqs; ++j)  // the same word for every thread: a broadcast
-        rank += keys[j] > key || (keys[j] == key && j < tid);
-    }
-    if (q_len > 1 && rank == z) {
-      sc.s = si;
-      sc.row0 = row0;
-      sc.q_len = q_len;
-      sc.L = L;
-    }
-    __syncthreads();
-  }
-  __syncthreads();
-  if (first && tid == 0 && found > a.prefill_seqs) atomicOr(a.err, kErrHint);
+__device__ __forceinline__ bool find_tile(const DiffArgs& a, ChunkScan<ChunkCfg::kThreads>& sc,
+                                          int* keys, int qt, int z, int split, bool first,
+                                          bool lead, Tile& t) {
+  const int tid = threadIdx.x;
+  find_chunk(a, sc, keys, z, first);
   t.s = sc.s;
   if (t.s < 0) return false;
   t.tile_q = 128 / a.group;
@@ -311,8 +267,9 @@ struct Maxima {
 // One score buffer's softmax by the 512 threads: this thread's row r, columns 32 cq .. + 31 of S at
 // sbuf.  The weights are taken against the row's base m so far.  Only where that does not do (no
 // base yet, or a thread's 32 weights sum to more than 2^10, so one is above 2^5: they stay far
-// below fp16's 2^16) are the maxima exchanged, O brought to the new base by `rebase` and the
-// weights taken again, from the scores still in TMEM.  So the usual tile computes no maximum, and
+// below fp16's 2^16) are the maxima of the threads that want it exchanged, O brought to the new
+// base by `rebase` and the weights taken again, from the scores still in TMEM; a row that does not
+// want one keeps its base, so no row's result depends on the rows beside it.  So the usual tile computes no maximum, and
 // the one meeting of the row's four threads only asks whether anyone wants a new base.  P goes
 // where the thread's own scores were: 16 columns from 32 cq on.  False, for all four of a row's
 // warps, when one of them had no scores (its wait gave up).
@@ -332,16 +289,15 @@ __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int 
       load_scores(sbuf + 32 * cq, sv, prescale, scale_log2, masked, key0, pos);
       sum = weigh<BF>(sv, pk, mul, m_run == -INFINITY ? 0.f : -m_run * mul);
     }
-    if (turn == 1 ||
-        !bar_sync_or(meet_bar, 128, !got || m_run == -INFINITY || !(sum <= 1024.f)))
-      break;
+    const bool wants = m_run == -INFINITY || !(sum <= 1024.f);
+    if (turn == 1 || !bar_sync_or(meet_bar, 128, !got || wants)) break;
     uint32_t up = 0x7fffff00u;  // NaN: this thread has given up (a maximum itself is never NaN)
     if (got) {
       load_scores(sbuf + 32 * cq, sv, prescale, scale_log2, masked, key0, pos);
       float top = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(sv[c]));
-      up = round_up24(top);
+      up = round_up24(wants ? top : -INFINITY);
     }
     mx.hi[cq][r] = static_cast<uint16_t>(up >> 16);
     mx.lo[cq][r] = static_cast<uint8_t>(up >> 8);
@@ -480,7 +436,7 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   __shared__ __align__(8) uint64_t v_full[C::kVStages], v_empty[C::kVStages];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, drain;
   __shared__ uint32_t tmem_base;
-  __shared__ TileScan scan;
+  __shared__ ChunkScan<C::kThreads> scan;
   __shared__ int softmax_stop;
   __shared__ Maxima maxima[2];  // per map
 
@@ -778,7 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   __shared__ uint32_t tmem_base;
   // the other CTA's rings may be written; the other map's rows have arrived
   __shared__ __align__(8) uint64_t peer_free, rows_in;
-  __shared__ TileScan scan;
+  __shared__ ChunkScan<C::kThreads> scan;
   __shared__ int softmax_stop;
   __shared__ Maxima maxima;
 

@@ -81,6 +81,81 @@ def test_matches_the_formula(name, bf16):
     check(run(b, lam, weight, gain=0.4), *diff_attention_ref(b, lam, weight, gain=0.4))
 
 
+SPLIT = {
+    # too few chunk tiles to fill the GPU: their keys are shared out and joined
+    "d128_g4": dict(specs=[(5000, 200)], hq=8, hkv=2, d=128),
+    "d64_g2": dict(specs=[(5000, 300), (2600, 20)], hq=4, hkv=2, d=64),
+    "d128_g3_beside_rows": dict(specs=[(6100, 260), (3000, 1), (40, 1)], hq=6, hkv=2, d=128),
+    "d64_g16_bs32": dict(specs=[(4100, 90)], hq=32, hkv=2, d=64, bs=32),
+}
+
+
+def split_batch(name):
+    c = SPLIT[name]
+    return W.build_batch("split_" + name, [W.SeqSpec(*x) for x in c["specs"]], num_q_heads=c["hq"],
+                         num_kv_heads=c["hkv"], head_dim=c["d"], block_size=c.get("bs", 16),
+                         seed_base=9230 + len(name))
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["f16", "bf16"])
+@pytest.mark.parametrize("name", list(SPLIT))
+def test_chunks_whose_keys_are_shared_out(name, bf16):
+    b = split_batch(name)
+    b = W.to_bf16(b) if bf16 else b
+    lam, weight = learned(b)
+    check(run(b, lam, weight), *diff_attention_ref(b, lam, weight))
+    check(run(b, lam, gain=0.5), *diff_attention_ref(b, lam, gain=0.5))
+
+
+@pytest.mark.parametrize("d, bs", [(128, 16), (64, 32)])
+def test_whole_prompts_alone(d, bs):
+    b = W.build_batch("prompts", [W.SeqSpec(900, 900), W.SeqSpec(400, 399), W.SeqSpec(129, 129)],
+                      num_q_heads=8, num_kv_heads=2, head_dim=d, block_size=bs, seed_base=9240)
+    lam, weight = learned(b)
+    check(run(b, lam, weight), *diff_attention_ref(b, lam, weight))
+
+
+def test_many_sequences():
+    """More sequences than the chunk kernel sorts, and than it has threads; some without rows."""
+    specs = [W.SeqSpec(1 + i % 5, i % 2) for i in range(700)]
+    specs[3], specs[650], specs[699] = W.SeqSpec(600, 512), W.SeqSpec(300, 257), W.SeqSpec(70, 9)
+    b = W.build_batch("many", specs, num_q_heads=2, num_kv_heads=2, head_dim=64, block_size=16,
+                      seed_base=9241)
+    lam, weight = learned(b)
+    check(run(b, lam, weight), *diff_attention_ref(b, lam, weight))
+
+
+def test_hidden_keys_of_the_chunk_do_not_reach_earlier_rows():
+    """A key that only later rows see may score anything; earlier rows are the same to the bit."""
+    b = W.build_batch("hidden", [W.SeqSpec(700, 600)], num_q_heads=8, num_kv_heads=2, head_dim=64,
+                      block_size=16, seed_base=9242)
+    lam, weight = learned(b)
+    first = run(b, lam, weight)
+    blk, off = int(b.block_tables[0, 650 // 16]), 650 % 16
+    b.k_cache[blk, :, off] = 3000.0
+    b.v_cache[blk, :, off] = -50000.0
+    again = run(b, lam, weight)
+    seen = 650 - (700 - 600)
+    assert torch.equal(first[:seen], again[:seen])
+    assert not torch.equal(first[seen:], again[seen:])
+
+
+def test_scores_that_rise_late():
+    """Each block of keys scores far above all before it, so the softmax base has to follow."""
+    b = W.build_batch("rising", [W.SeqSpec(900, 300), W.SeqSpec(1400, 1)], num_q_heads=4,
+                      num_kv_heads=2, head_dim=64, block_size=16, seed_base=9243)
+    step = torch.arange(1400) // 64
+    for s in range(2):
+        n, base = int(b.seq_lens[s]), int(b.kv_start[s])
+        for h in range(2):
+            b.k_contig[base:base + n, h] = (step[:n, None] * 3.0).half()
+        for i in range(n):
+            b.k_cache[int(b.block_tables[s, i // 16]), :, i % 16] = b.k_contig[base + i]
+    b.q[:] = b.q.abs()
+    lam, weight = learned(b)
+    check(run(b, lam, weight), *diff_attention_ref(b, lam, weight))
+
+
 def test_long_contexts():
     b = small_long_chunks(hq=4, hkv=2)
     lam, weight = learned(b)
@@ -207,6 +282,86 @@ def test_bad_descriptors_leave_rows_alone():
     out, (st, bits) = call(b.block_tables, b.seq_lens, 600)
     assert st == B.PA_ERR_DESCRIPTOR and bits & 16
     others(out, {8, 9})  # more than two partitions' keys
+
+
+def test_too_small_hints_are_reported():
+    """More chunks, or longer ones, than the hint says: reported, and the other rows are right."""
+    b = small_mixed(d=64, hq=16, hkv=4, seed=9226)
+    lam, weight = learned(b)
+    ref, bound = diff_attention_ref(b, lam, weight)
+    for rows, seqs in ((b.max_query_len, 3), (100, b.num_prefill_seqs)):
+        out = torch.full((b.num_tokens, 8, 128), float("nan"), dtype=b.q.dtype, device="cuda")
+        pa.diff_attention(b.q.cuda(), b.k_cache.cuda(), b.v_cache.cuda(), b.block_tables.cuda(),
+                          b.seq_lens.cuda(), b.query_start_loc.cuda(), b.scale, lam.cuda(), out,
+                          rows, b.max_seq_len, norm_weight=weight.cuda(), num_prefill_seqs=seqs)
+        st, bits = pa.get_device_error()
+        assert st == B.PA_ERR_DESCRIPTOR and bits & 16
+        out = out.cpu()
+        lost = out.isnan().all(-1).all(-1)
+        assert lost.any() and not lost.all()
+        check(out[~lost], ref[~lost], bound[~lost])
+
+
+@pytest.mark.parametrize("hint", [1, 2])
+def test_rows_beyond_the_hint_are_reported(hint):
+    """Calls that the rows kernel serves alone: a sequence with more rows than the hint allows."""
+    b = W.build_batch("beyond", [W.SeqSpec(40, 1), W.SeqSpec(50, 3), W.SeqSpec(300, 1)],
+                      num_q_heads=4, num_kv_heads=4, head_dim=64, block_size=16, seed_base=9244)
+    lam, weight = learned(b)
+    out = torch.full((5, 2, 128), float("nan"), dtype=b.q.dtype, device="cuda")
+    pa.diff_attention(b.q.cuda(), b.k_cache.cuda(), b.v_cache.cuda(), b.block_tables.cuda(),
+                      b.seq_lens.cuda(), b.query_start_loc.cuda(), b.scale, lam.cuda(), out, hint,
+                      b.max_seq_len, norm_weight=weight.cuda())
+    st, bits = pa.get_device_error()
+    assert st == B.PA_ERR_DESCRIPTOR and bits & 16
+    out = out.cpu()
+    assert out[1:4].isnan().all()
+    ref, bound = diff_attention_ref(b, lam, weight)
+    for row in (0, 4):
+        check(out[row], ref[row], bound[row])
+
+
+def test_bad_ids_in_shared_out_keys():
+    b = split_batch("d64_g2")
+    lam, weight = learned(b)
+    bad = b.block_tables.clone()
+    bad[0, 200] = b.num_blocks  # in one of the first sequence's ranges
+    out = torch.full((b.num_tokens, 2, 128), float("nan"), dtype=b.q.dtype, device="cuda")
+    pa.diff_attention(b.q.cuda(), b.k_cache.cuda(), b.v_cache.cuda(), bad.cuda(), b.seq_lens.cuda(),
+                      b.query_start_loc.cuda(), b.scale, lam.cuda(), out, b.max_query_len,
+                      b.max_seq_len, norm_weight=weight.cuda(), num_prefill_seqs=2)
+    st, bits = pa.get_device_error()
+    assert st == B.PA_ERR_OUT_OF_RANGE and bits & 4
+    assert out[:300].isnan().all()
+    ref, bound = diff_attention_ref(b, lam, weight, rows_of={1})
+    check(out[300:], ref[300:], bound[300:])
+
+
+@pytest.mark.parametrize("name", ["decode", "chunks"])
+def test_two_streams_at_once(name):
+    """Two calls in flight on streams of their own, each with its own workspace."""
+    b = small_decode(hq=8, hkv=4, d=64) if name == "decode" else split_batch("d64_g2")
+    lam, weight = learned(b)
+    ref, bound = diff_attention_ref(b, lam, weight)
+    dev = [x.cuda() for x in (b.q, b.k_cache, b.v_cache, b.block_tables, b.seq_lens,
+                              b.query_start_loc)]
+    lam, weight = lam.cuda(), weight.cuda()
+    torch.cuda.synchronize()
+    outs = []
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                out = torch.empty((b.num_tokens, b.num_q_heads // 2, 2 * b.head_dim),
+                                  dtype=b.q.dtype, device="cuda")
+            out.record_stream(s)
+            pa.diff_attention(*dev, b.scale, lam, out, b.max_query_len, b.max_seq_len,
+                              norm_weight=weight, num_prefill_seqs=b.num_prefill_seqs, stream=s)
+            outs.append(out)
+    torch.cuda.synchronize()
+    assert pa.get_device_error() == (0, 0)
+    for out in outs:
+        check(out, ref, bound)
 
 
 def test_bad_chunks_leave_their_rows_alone():
