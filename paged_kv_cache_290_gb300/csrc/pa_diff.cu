@@ -656,7 +656,8 @@ cudaError_t launch_diff_merge(const DiffArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_diff_chunk_merge(const DiffArgs& a, cudaStream_t stream) {
-  const int64_t work = static_cast<int64_t>(a.max_query_len) * (a.num_q_heads / 2);
+  const int64_t work = std::min<int64_t>(a.max_query_len, a.num_tokens) * (a.num_q_heads / 2);
+  if ((work + 1) / 2 > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>((work + 1) / 2), a.prefill_seqs);
   if (a.bf16)
     a.head_dim == 128 ? diff_chunk_merge_kernel<128, true><<<grid, 128, 0, stream>>>(a)
@@ -715,7 +716,8 @@ DiffPlan diff_plan(int64_t t, int64_t n, int64_t hq, int64_t hkv, int64_t d,
   p.key_splits = 1;
   if (p.chunks) {
     const int64_t tile_q = 128 / group;
-    const int64_t ctas = (hint.max_query_len + tile_q - 1) / tile_q * (hkv / 2) * p.prefill_seqs *
+    const int64_t rows = std::min<int64_t>(hint.max_query_len, t);
+    const int64_t ctas = (rows + tile_q - 1) / tile_q * (hkv / 2) * p.prefill_seqs *
                          (d == 128 ? 2 : 1);
     p.key_splits = static_cast<int>(
         std::max<int64_t>(1, std::min<int64_t>({kSms / ctas, parts_of(512), 32})));
