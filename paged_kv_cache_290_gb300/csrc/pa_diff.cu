@@ -1,4 +1,5 @@
-// Differential attention over a paged KV cache: rows of decode steps, and the entry point.
+// Differential attention over a paged KV cache: rows of decode steps and short chunks, the merges,
+// and the entry point.  Longer chunks: pa_diff_chunk.cu.
 //
 // Heads come in pairs.  Of q, heads 2p and 2p + 1 are the queries of the two softmax maps of
 // differential head p; of the pool, K heads 2j and 2j + 1 are the two maps' keys and V heads
@@ -9,8 +10,10 @@
 //   out = c y rsqrt(mean(y^2) + eps) w.
 // The subtraction is of two normalised sums, both float32; nothing is rounded before `out`.
 //
-// Rows kernel: CTA = (sequence, kv-head pair, partition of the keys).  One read of the four heads'
-// K/V units serves every (query row, head) column of the pair and both maps.  Bound by HBM.
+// Rows kernel: CTA = (sequence, kv-head pair, 4 or 8 columns, partition of the keys), a column being
+// a (query row, head).  One read of the four heads' K/V units serves all of its columns and both
+// maps.  Bound by HBM: 32 rows behind 8192 keys (64 + 8 heads of 128) 167.8 us = 6.41 TB/s, 0.96 of
+// the measured copy rate; 64 rows behind 512 to 4096 keys 94.7 us = 6.58 TB/s.
 //   * a warp streams 16-token units (K1, K2, Va, Vb: 4 x 16 x d values, two copies) through its
 //     own ring of 2 TMA stages, or 3 or 6 where a small grid leaves the SM's shared memory free
 //     (one sequence of 4096 keys: 17 -> 11 us with the partitions below);
@@ -19,7 +22,8 @@
 //     4-7 map 2: each K's product with the whole tile, of which its own half is kept, so that one
 //     P V product serves both maps); NT = 2 has 8 columns, a tile per map.
 //   * online softmax per column as in the decode kernel (a reference maximum raised only past
-//     2^8), scores masked by a select, V rows past the sequence's end zeroed.
+//     2^8), scores masked by a select, V rows past the sequence's end zeroed.  Each weight goes into
+//     the product as two numbers, its rounding and the rest, so only `out` is rounded.
 // A sequence within one partition is finished in the CTA; otherwise (m, l, O / l) partials of
 // both maps go to the workspace and the merge kernel joins them (log-sum-exp), subtracts and
 // normalises.
@@ -58,14 +62,6 @@ struct RowsCfg {
   static_assert(kMergeBytes <= 2 * kWarps * kStageBytes, "the warps' sums fit the rings");
   static constexpr float kRaiseLog2 = 8.f;
 };
-
-template <bool BF>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if constexpr (BF)
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  else
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
 
 // y of one differential head (kV consecutive dims per lane, a warp per head) -> out.
 template <int D, bool BF>

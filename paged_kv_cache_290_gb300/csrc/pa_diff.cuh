@@ -1,10 +1,19 @@
-// Device code shared by the chunk kernels of differential attention and the merge behind them.
+// Device code that the rows kernel, the chunk kernels and the merges of differential attention share.
 #pragma once
 
 #include "pa_common.cuh"
 #include "pa_diff.h"
 
 namespace pa {
+
+// The two element-type values of a word.
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 
 // A block's search for its chunk: the descriptor found (s = -1: none).
 template <int kThreads>

@@ -21,6 +21,13 @@
 //     (row, quarter of the tile's columns), while the pipe works on the other buffer.  The base m
 //     of a row is raised only when weights against it grow large (then O is rescaled in TMEM).
 // Every wait is bounded; V rows past the last visible key are zeroed before their product.
+//
+// Bound by the tensor pipe and the softmax about it: a key tile takes 1.13 us a map at d = 128 and
+// 1.35 us for both maps at d = 64 (its products alone, with the rests below, 1.17 us each at the
+// measured rate of large matrix products); and by what surrounds the key loop, about 12 us a CTA
+// (search, first loads, first tile, end) in which the pipe idles, since an SM holds one CTA.  4 x 512
+// rows behind up to 7.5k keys (32 + 8 heads of 128): 192 us = 1130 TFLOP/s, 0.59 of the measured
+// burst; a prompt of 4001 rows (32 + 8 heads of 64): 112 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -204,10 +211,14 @@ __device__ __forceinline__ void load_scores(uint32_t addr, uint32_t (&sv)[32], b
 // Their weights 2^(score mul + neg_m), rounded to the element type for the matrix product (at most
 // 2^-11 (fp16) or 2^-8 (bf16) of each weight, at random over the keys), two keys a word; returns
 // the unrounded weights' sum.  (Summing the rounded weights instead changes the result's error by
-// under 1%.)
+// under 1%.)  What the rounding took off the first 8 goes into `rest` in the same form and through a
+// product of its own: a quarter of the weights enter to twice the bits.  The result's error against
+// 64 bits falls from 1.53 to 1.46 times that of the output's own rounding (bf16, 32 + 8 heads of
+// 128; the maps' difference magnifies it), for 1.03 -> 1.13 us a tile at d = 128 and 1.21 -> 1.35 at
+// d = 64; all of them would take twice the products of P and V.
 template <bool BF>
-__device__ __forceinline__ float weigh(const uint32_t (&sv)[32], uint32_t (&pk)[16], float mul,
-                                       float neg_m) {
+__device__ __forceinline__ float weigh(const uint32_t (&sv)[32], uint32_t (&pk)[16],
+                                       uint32_t (&rest)[4], float mul, float neg_m) {
   const uint64_t mul2 = f32x2(mul, mul), negm2 = f32x2(neg_m, neg_m);
   uint64_t ps2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll
@@ -218,6 +229,10 @@ __device__ __forceinline__ float weigh(const uint32_t (&sv)[32], uint32_t (&pk)[
     const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
     ps2[(k >> 1) & 1] = fadd2(ps2[(k >> 1) & 1], f32x2(p0, p1));
     pk[k >> 1] = pack2<BF>(p0, p1);
+    if (k < 8) {
+      const float2 w = unpack2<BF>(pk[k >> 1]);
+      rest[k >> 1] = pack2<BF>(p0 - w.x, p1 - w.y);
+    }
   }
   float s0, s1, s2, s3;
   f32x2_split(ps2[0], s0, s1);
@@ -266,19 +281,20 @@ struct Maxima {
 
 // One score buffer's softmax by the 512 threads: this thread's row r, columns 32 cq .. + 31 of S at
 // sbuf.  The weights are taken against the row's base m so far.  Only where that does not do (no
-// base yet, or a thread's 32 weights sum to more than 2^10, so one is above 2^5: they stay far
-// below fp16's 2^16) are the maxima of the threads that want it exchanged, O brought to the new
-// base by `rebase` and the weights taken again, from the scores still in TMEM; a row that does not
-// want one keeps its base, so no row's result depends on the rows beside it.  So the usual tile computes no maximum, and
-// the one meeting of the row's four threads only asks whether anyone wants a new base.  P goes
-// where the thread's own scores were: 16 columns from 32 cq on.  False, for all four of a row's
-// warps, when one of them had no scores (its wait gave up).
+// base yet, or a thread's 32 weights sum to more than 2^10, so one is above 2^5: they stay far below
+// fp16's 2^16) are the maxima of the threads that want it exchanged, O brought to the new base by
+// `rebase` and the weights taken again, from the scores still in TMEM; a row that does not want one
+// keeps its base, so no row's result depends on the rows beside it.  So the usual tile computes no
+// maximum, and the one meeting of the row's four threads only asks whether anyone wants a new base.
+// P goes where the thread's own scores were: 16 columns from 32 cq on.  The rests of the first 8
+// weights of quarters 0 and 1 stand together behind P of quarter 0, those of 2 and 3 behind quarter
+// 2's.  False, for all four of a row's warps, when one of them had no scores (its wait gave up).
 template <bool BF, typename Rebase>
 __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int r, int cq,
                                        uint32_t meet_bar, bool prescale, float scale_log2,
                                        bool masked, int key0, int pos, float mul, float& m_run,
                                        float& l_run, Rebase rebase) {
-  uint32_t pk[16];
+  uint32_t pk[16], rest[4];
   float sum = 0.f;
   // Unrolled, so that the usual tile runs straight through (a 4001-row prompt 111 -> 105 us).
 #pragma unroll 2
@@ -287,10 +303,11 @@ __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int 
     if (got) {
       tmem_fence_after_sync();
       load_scores(sbuf + 32 * cq, sv, prescale, scale_log2, masked, key0, pos);
-      sum = weigh<BF>(sv, pk, mul, m_run == -INFINITY ? 0.f : -m_run * mul);
+      sum = weigh<BF>(sv, pk, rest, mul, m_run == -INFINITY ? 0.f : -m_run * mul);
     }
     const bool wants = m_run == -INFINITY || !(sum <= 1024.f);
-    if (turn == 1 || !bar_sync_or(meet_bar, 128, !got || wants)) break;
+    // (the second time: everyone's scores are read before anyone's rests are stored)
+    if (!bar_sync_or(meet_bar, 128, turn == 0 && (!got || wants))) break;
     uint32_t up = 0x7fffff00u;  // NaN: this thread has given up (a maximum itself is never NaN)
     if (got) {
       load_scores(sbuf + 32 * cq, sv, prescale, scale_log2, masked, key0, pos);
@@ -321,6 +338,7 @@ __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int 
   }
   l_run += sum;
   tmem_st16(sbuf + 32 * cq, pk);
+  tmem_st4(sbuf + 64 * (cq >> 1) + 16 + 4 * (cq & 1), rest);
   return true;
 }
 
@@ -566,7 +584,9 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
           if (!ok) break;
           p_seen = false;
 #pragma unroll
-          for (int k = 0; k < C::kKeys / 16; ++k) {
+          for (int k = 0; k < C::kKeys / 16 + 2; ++k) {
+            // the last two: the rests of 8 keys each of two quarters, 32 keys apart in V
+            const int rest = k - C::kKeys / 16;
             if (k == 6 && more) {
               if (t == 0)
                 k_seen = test(k_bar(j + 1), (j + 1) / C::kKStages & 1);
@@ -574,8 +594,11 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
                 v_seen = test(v_bar(j + 1), (j + 1) / C::kVStages & 1);
             }
             umma_f16_tmem_a_if(leader, tmem + C::kOCol + t * 128,
-                               tmem + t * 128 + (k >> 1) * 32 + (k & 1) * 8,
-                            umma_sdesc(vb + k * 4096, 2048, 1024), kIdO, (j > 0 || k > 0));
+                               tmem + t * 128 +
+                                   (rest < 0 ? (k >> 1) * 32 + (k & 1) * 8 : rest * 64 + 16),
+                               rest < 0 ? umma_sdesc(vb + k * 4096, 2048, 1024)
+                                        : umma_sdesc(vb + rest * 4 * 4096, 2048, 2 * 4096),
+                               kIdO, (j > 0 || k > 0));
           }
           if (t == 1) umma_commit_if(leader, smem_addr(&v_empty[vst]));
           if (more) {
@@ -862,11 +885,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
         v_seen = p_seen = false;
         const uint32_t vb = v_s + vst * C::kVBytes;
 #pragma unroll
-        for (int k = 0; k < C::kKeys / 16; ++k) {
+        for (int k = 0; k < C::kKeys / 16 + 2; ++k) {
+          // the last two: the rests of 8 keys each of two quarters, 32 keys apart in V
+          const int rest = k - C::kKeys / 16;
           if (k == 6 && more) k_seen = test(k_bar(j + 2), (j + 2) / C::kKStages & 1);
           umma_f16_tmem_a_if(leader, tmem + C::kOCol,
-                             tmem + (j & 1) * 128 + (k >> 1) * 32 + (k & 1) * 8,
-                          umma_sdesc(vb + k * 8192, 2048, 1024), kIdO, (j > 0 || k > 0));
+                             tmem + (j & 1) * 128 +
+                                 (rest < 0 ? (k >> 1) * 32 + (k & 1) * 8 : rest * 64 + 16),
+                             rest < 0 ? umma_sdesc(vb + k * 8192, 2048, 1024)
+                                      : umma_sdesc(vb + rest * 4 * 8192, 2048, 2 * 8192),
+                             kIdO, (j > 0 || k > 0));
         }
         umma_commit_if(leader, smem_addr(&v_empty[vst]));
         if (more) {
@@ -1129,7 +1157,7 @@ cudaError_t launch_t(K kern, std::atomic<uint64_t>& done, const DiffArgs& a,
   if (e != cudaSuccess) return e;
   // Grid x: Q tiles, the last of a chunk (with the most keys) first, every pair of one before the
   // next: longest first over all pairs, so that the grid's tail is short (2432 rows, 32 + 8 heads
-  // of 64, 49.2 us against 58.4 with one pair after the other; 4 x 512 rows, heads of 128, 177
+  // of 64, 49 us against 58 with one pair after the other; 4 x 512 rows, heads of 128, 177
   // against 180).
   const int tile_q = C::kRows / a.group;
   const int64_t rows = std::min<int64_t>(a.max_query_len, a.num_tokens);
