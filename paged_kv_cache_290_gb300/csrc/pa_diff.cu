@@ -747,9 +747,11 @@ extern "C" {
 size_t pa_diff_attention_workspace_size(int64_t num_tokens, int64_t num_seqs, int64_t num_q_heads,
                                         int64_t num_kv_heads, int64_t head_dim,
                                         const pa_batch_hint* hint) {
-  if (!hint || num_tokens <= 0 || num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads < num_kv_heads ||
-      head_dim <= 0 || hint->max_query_len <= 0 || hint->max_seq_len < 0)
-    return 0;
+  if (!hint || num_tokens <= 0 || num_seqs <= 0 || num_kv_heads < 2 || num_kv_heads % 2 != 0 ||
+      num_q_heads < num_kv_heads || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > 16 || head_dim <= 0 || hint->max_query_len <= 0 ||
+      hint->max_seq_len < 0)
+    return 0;  // nothing to do, or refused by the call itself
   return pa::diff_plan(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, *hint).total;
 }
 

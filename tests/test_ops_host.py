@@ -138,6 +138,13 @@ def test_diff_refuses(lib, kw, status, text):
     assert text in msg(lib), msg(lib)
 
 
+@pytest.mark.parametrize("hq, hkv", [(1024, 2), (6, 3), (8, 1), (7, 2), (0, 2), (2, 4)])
+def test_diff_workspace_of_refused_heads_is_empty(lib, hq, hkv):
+    h = B.PABatchHint(512, 4096, 4, 0)
+    assert lib.pa_diff_attention_workspace_size(4096, 8, hq, hkv, 128, ctypes.byref(h)) == 0
+    assert lib.pa_diff_attention_workspace_size(4096, 8, 8, 2, 128, ctypes.byref(h)) > 0
+
+
 def test_diff_without_rows_is_a_no_op(lib):
     assert call_diff(lib, q=T(B.PA_F16, [0, 8, 64]), out=T(B.PA_F16, [0, 4, 128]),
                      hint=(0, 0)) == B.PA_OK
