@@ -51,10 +51,12 @@ __device__ __forceinline__ void find_chunk(const DiffArgs& a, ChunkScan<kThreads
     if (sorted && tid < 128) keys[tid] = key;
     __syncthreads();
     int rank = found + __popc(bal & ((1u << lane) - 1u));
+    if (!sorted || first) {
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      rank += w < warp ? sc.warp_count[w] : 0;
-      found += sc.warp_count[w];
+      for (int w = 0; w < kThreads / 32; ++w) {
+        rank += w < warp ? sc.warp_count[w] : 0;
+        found += sc.warp_count[w];
+      }
     }
     if (sorted && q_len > 1) {
       rank = 0;

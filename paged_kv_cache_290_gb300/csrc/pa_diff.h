@@ -20,6 +20,9 @@ struct DiffArgs : AttnArgs {
   int group_inv;         // 65536 / group + 1
   int stages;            // units in flight per warp of the rows kernel
   int max_seq_len;       // the hint's
+  int tile_q;            // query rows of a chunk tile: 128 / group
+  int chunk_tiles;       // chunk tiles of the longest chunk
+  uint32_t pairs_inv;    // ceil(2^32 / num_pairs)
   int key_splits;        // ranges of the keys that the chunk kernel's CTAs share out
   float* chunk_o;        // partials of the chunk kernel: [T, Hq, key_splits, 2 d]
   float* chunk_m;        // [T, Hq, key_splits], log2 units

@@ -91,18 +91,36 @@ struct Tile {
   int key_stop, ntiles;
 };
 
+// The CTA's place: grid x is (tile from the last on, kv-head pair), z (rank of the chunk, key range).
+struct Place {
+  int pair, back, z, split;
+};
+__device__ __forceinline__ Place place_of(const DiffArgs& a, unsigned x) {
+  Place p;
+  p.back = static_cast<int>(a.num_pairs > 1 ? __umulhi(x, a.pairs_inv) : x);
+  p.pair = static_cast<int>(x) - p.back * a.num_pairs;
+  p.z = blockIdx.z;
+  p.split = 0;
+  if (a.key_splits > 1) {
+    p.split = p.z % a.key_splits;
+    p.z /= a.key_splits;
+  }
+  return p;
+}
+
 // Finds and checks the tile; false when the CTA has none (errors are reported).  All threads of
 // the block call it.  keys: 128 words that nothing uses yet (of Q's tile, which only generic
 // stores fill).
 template <int BS>
 __device__ __forceinline__ bool find_tile(const DiffArgs& a, ChunkScan<ChunkCfg::kThreads>& sc,
-                                          int* keys, int qt, int z, int split, bool first,
-                                          bool lead, Tile& t) {
+                                          int* keys, const Place& at, Tile& t) {
+  const bool lead = blockIdx.x == 0 && at.split == 0, first = blockIdx.x == 0 && blockIdx.z == 0;
+  const int qt = a.chunk_tiles - 1 - at.back, split = at.split;
   const int tid = threadIdx.x;
-  find_chunk(a, sc, keys, z, first);
+  find_chunk(a, sc, keys, at.z, first);
   t.s = sc.s;
   if (t.s < 0) return false;
-  t.tile_q = 128 / a.group;
+  t.tile_q = a.tile_q;
   t.row0 = sc.row0;
   t.q_len = sc.q_len;
   const int L = sc.L;
@@ -120,7 +138,9 @@ __device__ __forceinline__ bool find_tile(const DiffArgs& a, ChunkScan<ChunkCfg:
   t.ctx = L - t.q_len;
   t.kend = t.ctx + min(t.q_len, t.qbase + t.tile_q);
   const int all_tiles = (t.kend + 127) / 128;
-  const int per = (all_tiles + a.key_splits - 1) / a.key_splits;
+  // (divisions cost a CTA's start 0.2 us each; so the host's inverses, and none for one range)
+  const int per =
+      a.key_splits > 1 ? (all_tiles + a.key_splits - 1) / a.key_splits : all_tiles;
   t.ntiles = min(all_tiles - split * per, per);
   if (t.ntiles <= 0) return false;
   t.key_base = split * per * 128;
@@ -280,7 +300,8 @@ struct Maxima {
 };
 
 // One score buffer's softmax by the 512 threads: this thread's row r, columns 32 cq .. + 31 of S at
-// sbuf.  The weights are taken against the row's base m so far.  Only where that does not do (no
+// sbuf (fresh: the first, for which there is no base).  The weights are taken against the row's base
+// m so far.  Only where that does not do (no
 // base yet, or a thread's 32 weights sum to more than 2^10, so one is above 2^5: they stay far below
 // fp16's 2^16) are the maxima of the threads that want it exchanged, O brought to the new base by
 // `rebase` and the weights taken again, from the scores still in TMEM; a row that does not want one
@@ -292,24 +313,25 @@ struct Maxima {
 template <bool BF, typename Rebase>
 __device__ __forceinline__ bool soften(uint32_t sbuf, bool got, Maxima& mx, int r, int cq,
                                        uint32_t meet_bar, bool prescale, float scale_log2,
-                                       bool masked, int key0, int pos, float mul, float& m_run,
-                                       float& l_run, Rebase rebase) {
+                                       bool masked, int key0, int pos, float mul, bool fresh,
+                                       float& m_run, float& l_run, Rebase rebase) {
   uint32_t pk[16], rest[4];
   float sum = 0.f;
   // Unrolled, so that the usual tile runs straight through (a 4001-row prompt 111 -> 105 us).
 #pragma unroll 2
   for (int turn = 0; turn < 2; ++turn) {
     uint32_t sv[32];
-    if (got) {
+    if (got && !(turn == 0 && fresh)) {
       tmem_fence_after_sync();
       load_scores(sbuf + 32 * cq, sv, prescale, scale_log2, masked, key0, pos);
       sum = weigh<BF>(sv, pk, rest, mul, m_run == -INFINITY ? 0.f : -m_run * mul);
     }
-    const bool wants = m_run == -INFINITY || !(sum <= 1024.f);
+    const bool wants = m_run == -INFINITY || !(sum <= 1024.f);  // at first: everyone
     // (the second time: everyone's scores are read before anyone's rests are stored)
     if (!bar_sync_or(meet_bar, 128, turn == 0 && (!got || wants))) break;
     uint32_t up = 0x7fffff00u;  // NaN: this thread has given up (a maximum itself is never NaN)
     if (got) {
+      tmem_fence_after_sync();
       load_scores(sbuf + 32 * cq, sv, prescale, scale_log2, masked, key0, pos);
       float top = -INFINITY;
 #pragma unroll
@@ -465,11 +487,11 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   const uint32_t v_s = k_s + C::kKStages * C::kStageBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const int nsplit = a.key_splits, pair = blockIdx.x % a.num_pairs, qx = blockIdx.x / a.num_pairs;
-  const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
+  const Place at = place_of(a, blockIdx.x);
+  const int nsplit = a.key_splits, pair = at.pair, split = at.split;
   // Barriers and TMEM are set up while the search for the tile waits for its loads.
   if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
-  if (tid == 0) {
+  if (tid == 32) {  // beside the warp that allocates
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(smem_addr(&k_full[i]), 1);
       mbar_init(smem_addr(&k_empty[i]), 1);
@@ -489,9 +511,7 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
   }
   tmem_fence_before_sync();
   Tile tile;
-  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), gridDim.x / a.num_pairs - 1 - qx, z, split,
-                     blockIdx.x == 0 && blockIdx.z == 0,
-                     blockIdx.x == 0 && split == 0, tile)) {
+  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), at, tile)) {
     if (warp == 0) free_tmem(tmem_base, C::kTmemCols);
     return;
   }
@@ -651,7 +671,8 @@ __global__ void __launch_bounds__(BothCfg::kThreads, 1)
           if (j > 0) rescale(obuf + t * 128 + cq * (D / 2), D / 2, alpha);
         };
         if (!soften<BF>(tmem + lane_addr + t * 128, got, maxima[t], r, cq, 1 + quarter, prescale,
-                        a.scale_log2, masked, key0, pos, mul, m_run[t], l_run[t], rebase)) {
+                        a.scale_log2, masked, key0, pos, mul, j == 0,
+                        m_run[t], l_run[t], rebase)) {
           stopped = true;  // the row's four warps leave together
           break;
         }
@@ -768,12 +789,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   const uint32_t v_s = k_s + C::kKStages * C::kTileBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  const Place at = place_of(a, blockIdx.x >> 1);
   const int map = blockIdx.x & 1, nsplit = a.key_splits;  // map = cluster rank
-  const int pair = (blockIdx.x >> 1) % a.num_pairs, qx = (blockIdx.x >> 1) / a.num_pairs;
-  const int split = blockIdx.z % nsplit, z = blockIdx.z / nsplit;
+  const int pair = at.pair, split = at.split;
   // Barriers and TMEM are set up while the search for the tile waits for its loads.
   if (warp == 0) alloc_tmem(&tmem_base, C::kTmemCols);
-  if (tid == 0) {
+  if (tid == 32) {  // beside the warp that allocates
     for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(smem_addr(&k_full[i]), 1);
       mbar_init(smem_addr(&k_empty[i]), 1);
@@ -797,9 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
   tmem_fence_before_sync();
   Tile tile;
   // both CTAs of the cluster see the same tile: they leave early together or not at all
-  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), (gridDim.x >> 1) / a.num_pairs - 1 - qx, z, split,
-                     blockIdx.x == 0 && blockIdx.z == 0,
-                     blockIdx.x == 0 && split == 0, tile)) {
+  if (!find_tile<BS>(a, scan, reinterpret_cast<int*>(smem), at, tile)) {
     if (warp == 0) free_tmem(tmem_base, C::kTmemCols);
     return;
   }
@@ -950,8 +969,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MapCfg::kThreads, 1)
         if (!done) softmax_stop = 1;  // no row is written
       };
       if (!soften<BF>(tmem + lane_addr + (j & 1) * 128, got, maxima, r, cq, 1 + quarter, prescale,
-                      a.scale_log2, key0 + 31 > tile.ctx + tile.qbase, key0, pos, mul, m_run, l_run,
-                      rebase)) {
+                      a.scale_log2, key0 + 31 > tile.ctx + tile.qbase, key0, pos, mul, j == 0,
+                      m_run, l_run, rebase)) {
         stopped = true;  // the row's four warps leave together
         break;
       }
@@ -1159,12 +1178,17 @@ cudaError_t launch_t(K kern, std::atomic<uint64_t>& done, const DiffArgs& a,
   // next: longest first over all pairs, so that the grid's tail is short (2432 rows, 32 + 8 heads
   // of 64, 49 us against 58 with one pair after the other; 4 x 512 rows, heads of 128, 177
   // against 180).
-  const int tile_q = C::kRows / a.group;
+  DiffArgs b = a;
+  b.tile_q = C::kRows / a.group;
   const int64_t rows = std::min<int64_t>(a.max_query_len, a.num_tokens);
-  const int64_t ctas = (rows + tile_q - 1) / tile_q * a.num_pairs * ctas_per_tile;
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(ctas), 1, a.prefill_seqs * a.key_splits);
-  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(kmap, vmap, a);
+  const int64_t tiles = (rows + b.tile_q - 1) / b.tile_q, ctas = tiles * a.num_pairs;
+  // x / num_pairs as a multiplication: exact while x num_pairs < 2^32
+  if (ctas * a.num_pairs > UINT32_MAX || ctas * ctas_per_tile > INT32_MAX)
+    return cudaErrorInvalidConfiguration;
+  b.chunk_tiles = static_cast<int>(tiles);
+  b.pairs_inv = static_cast<uint32_t>(((uint64_t{1} << 32) + a.num_pairs - 1) / a.num_pairs);
+  const dim3 grid(static_cast<unsigned>(ctas * ctas_per_tile), 1, a.prefill_seqs * a.key_splits);
+  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(kmap, vmap, b);
   return cudaGetLastError();
 }
 
