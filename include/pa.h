@@ -328,7 +328,8 @@ int pa_rope_and_cache(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v
  *   workspace        device scratch of pa_diff_attention_workspace_size(...) bytes for the same
  *                    tokens (T), sequences (N), heads and hint; 256-byte aligned.
  * Rows of sequences that the device finds invalid are left unwritten and reported, as in
- * pa_attention.  The weights of a row's hidden keys are 0, but a V value of NaN or infinity at a
+ * pa_attention.  Accumulation is float32; a row's result depends on the batch's sizes (how its keys
+ * are split) to rounding, not on other rows or on page order.  The weights of a row's hidden keys are 0, but a V value of NaN or infinity at a
  * key that some row of the same chunk sees may reach the chunk's other rows (0 * infinity).
  * Supported: d in {64, 128}, bs in {16, 32}, Hq / Hkv in 1..16; not over FP8 pools.
  */
@@ -339,6 +340,7 @@ typedef struct pa_diff {
   float out_scale;
 } pa_diff;
 
+/* 0 also for heads that the call refuses. */
 size_t pa_diff_attention_workspace_size(int64_t num_tokens, int64_t num_seqs, int64_t num_q_heads,
                                         int64_t num_kv_heads, int64_t head_dim,
                                         const pa_batch_hint* hint);

@@ -22,12 +22,14 @@
 //     of a row is raised only when weights against it grow large (then O is rescaled in TMEM).
 // Every wait is bounded; V rows past the last visible key are zeroed before their product.
 //
-// Bound by the tensor pipe and the softmax about it: a key tile takes 1.13 us a map at d = 128 and
+// Bound by the tensor pipe and the softmax about it: a key tile takes 1.10 us a map at d = 128 and
 // 1.35 us for both maps at d = 64 (its products alone, with the rests below, 1.17 us each at the
-// measured rate of large matrix products); and by what surrounds the key loop, about 12 us a CTA
-// (search, first loads, first tile, end) in which the pipe idles, since an SM holds one CTA.  4 x 512
-// rows behind up to 7.5k keys (32 + 8 heads of 128): 192 us = 1130 TFLOP/s, 0.59 of the measured
-// burst; a prompt of 4001 rows (32 + 8 heads of 64): 112 us.
+// measured rate of large matrix products); and by what surrounds the key loop, about 10 us a CTA
+// (search 2, first loads and first tile 4, last products and end 5, overlapping little), in which
+// the pipe idles, since an SM holds one CTA.  4 x 512 rows behind up to 7.5k keys (32 + 8 heads of
+// 128): 182 us = 1200 TFLOP/s, 0.63 of the measured burst; a prompt of 4001 rows (32 + 8 heads of
+// 64): 107 us.  At d = 128 the key loop's speed hangs on its spills: versions with 32 more bytes
+// spilled took 5% longer.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -234,7 +236,7 @@ __device__ __forceinline__ void load_scores(uint32_t addr, uint32_t (&sv)[32], b
 // under 1%.)  What the rounding took off the first 8 goes into `rest` in the same form and through a
 // product of its own: a quarter of the weights enter to twice the bits.  The result's error against
 // 64 bits falls from 1.53 to 1.46 times that of the output's own rounding (bf16, 32 + 8 heads of
-// 128; the maps' difference magnifies it), for 1.03 -> 1.13 us a tile at d = 128 and 1.21 -> 1.35 at
+// 128; the maps' difference magnifies it), for 1.03 -> 1.10 us a tile at d = 128 and 1.21 -> 1.35 at
 // d = 64; all of them would take twice the products of P and V.
 template <bool BF>
 __device__ __forceinline__ float weigh(const uint32_t (&sv)[32], uint32_t (&pk)[16],
