@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <new>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "pa.h"
@@ -37,7 +38,7 @@ constexpr int kGroup = 32;
 constexpr int kMaxMoves = 1024, kFewMoves = 256;
 constexpr int kThreads = 256;  // of the renaming
 // Moves and bytes of a page per CTA: a list with chains keeps the plan's groups together; one
-// without takes smaller groups of longer slices, which start sooner (48 moves 5.8 -> 4.4 us, 1501
+// without takes smaller groups of longer slices, which start sooner (48 moves 1.3 us less, 1501
 // holes of an FP8 pool 67 -> 64.5 us).
 constexpr int kLooseGroup = 8, kSlice = 1024, kLooseSlice = 2048;
 static_assert(kMaxMoves % kGroup == 0 && kFewMoves % kGroup == 0, "a group lies in one launch");
@@ -53,14 +54,57 @@ struct MoveArgs {
   int layer0, layers;    // the batch of layers this launch covers
   int group, slice;      // moves, and bytes of a page, of a CTA
   int n;
-  int32_t* old_ids;      // tables: the move's old and new id by position, and a page's position
-  int32_t* new_ids;
+  int32_t* old_ids;      // long lists with tables: the move's old and new id by position, and a
+  int32_t* new_ids;      // page's position
   int32_t* position;
   int base;              // position of this launch's first move
+  int32_t* tables;       // short lists: [rows, cols], renamed by the grid's last z plane
+  int64_t rows, stride;
+  int cols;
   int32_t src[N];  // page id, or ~slot of the workspace
   int32_t dst[N];  // page id, or ~slot
   int32_t id[N];   // the moved page's old id
 };
+
+// Block tables after a short list of moves (at most kFewMoves): old ids and their new ones in a hash
+// table in shared memory (2 kFewMoves places of (id, new id), which the moves fill at most by half),
+// built by every block that renames.  Nothing here waits for the moves themselves.
+template <int N>
+__device__ __forceinline__ void rename_few(const MoveArgs<N>& a, int2* hash, int64_t first,
+                                           int64_t step) {
+  constexpr int kBits = 9;
+  static_assert((1 << kBits) == 2 * kFewMoves, "half full at most");
+  constexpr int kPlaces = 1 << kBits;
+  auto place = [](int32_t id) { return (static_cast<uint32_t>(id) * 0x9E3779B1u) >> (32 - kBits); };
+  for (int i = threadIdx.x; i < kPlaces; i += blockDim.x) hash[i] = make_int2(-1, -1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
+    uint32_t p = place(a.id[i]);
+    while (atomicCAS(&hash[p].x, -1, a.id[i]) != -1) p = (p + 1) % kPlaces;  // ids are distinct
+    hash[p].y = a.dst[i];
+  }
+  __syncthreads();
+  const int64_t total = a.rows * a.cols;
+  for (int64_t i = first; i < total; i += step) {
+    const int64_t row = total <= INT32_MAX ? static_cast<int>(i) / a.cols : i / a.cols;
+    int32_t* e = a.tables + row * a.stride + (i - row * a.cols);
+    const int32_t id = *e;
+    if (id < 0) continue;  // padding
+    for (uint32_t p = place(id); hash[p].x >= 0; p = (p + 1) % kPlaces)
+      if (hash[p].x == id) {
+        *e = hash[p].y;
+        break;
+      }
+  }
+}
+
+// The renaming alone, where the tables are too long for the blocks that move.
+__global__ void __launch_bounds__(kThreads)
+    rename_few_kernel(const __grid_constant__ MoveArgs<kFewMoves> a) {
+  __shared__ int2 hash[2 * kFewMoves];
+  rename_few(a, hash, static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x,
+             static_cast<int64_t>(gridDim.x) * kThreads);
+}
 
 template <int N>
 __global__ void __launch_bounds__(32) move_kernel(const __grid_constant__ MoveArgs<N> a) {
@@ -69,6 +113,14 @@ __global__ void __launch_bounds__(32) move_kernel(const __grid_constant__ MoveAr
   const int g0 = static_cast<int>(blockIdx.y) * a.group, n = min(a.group, a.n - g0);
   const int lz = static_cast<int>(blockIdx.z) >> 1, kv = static_cast<int>(blockIdx.z) & 1;
   const int lane = threadIdx.x;
+  if constexpr (N == kFewMoves)
+    if (lz == a.layers) {
+      const int64_t cta = blockIdx.y * gridDim.x + blockIdx.x;
+      if (cta * 32 < a.rows * a.cols)
+        rename_few(a, reinterpret_cast<int2*>(buf), cta * 32 + lane,
+                   static_cast<int64_t>(gridDim.x) * gridDim.y * 32);
+      return;
+    }
   if (a.position && blockIdx.x == 0 && blockIdx.z == 0)
     for (int i = lane; i < n; i += 32) {
       a.old_ids[a.base + g0 + i] = a.id[g0 + i];
@@ -110,7 +162,7 @@ __global__ void __launch_bounds__(32) move_kernel(const __grid_constant__ MoveAr
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// A moved page's id is replaced.  `position` is meaningful for moved pages only: any other entry
+// A moved page's id is replaced, after a long list.  `position` is meaningful for moved pages only: any other entry
 // holds whatever the workspace held, and is told apart by old_ids.
 __global__ void __launch_bounds__(kThreads)
     rename_kernel(int32_t* tables, int64_t rows, int cols, int64_t stride, int64_t num_blocks, int n,
@@ -174,6 +226,7 @@ void make_plan(pa_move_plan* p, const int32_t* pairs, int64_t n) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t rename_bytes(const pa_move_plan* p) {
+  if (p->dst.size() <= static_cast<size_t>(pa::kFewMoves)) return 0;
   return 2 * up256(p->dst.size() * sizeof(int32_t)) +
          up256(static_cast<size_t>(p->num_blocks) * sizeof(int32_t));
 }
@@ -311,10 +364,11 @@ int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_
   int64_t batch = per_layer ? static_cast<int64_t>((workspace_bytes - fixed) / per_layer) : layers;
   batch = std::min<int64_t>(std::max<int64_t>(batch, 1), layers);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int32_t* old_ids = tables ? reinterpret_cast<int32_t*>(ws) : nullptr;
-  int32_t* new_ids = tables ? reinterpret_cast<int32_t*>(ws + up256(n * sizeof(int32_t))) : nullptr;
+  const bool few = n <= kFewMoves, listed = tables && !few;
+  int32_t* old_ids = listed ? reinterpret_cast<int32_t*>(ws) : nullptr;
+  int32_t* new_ids = listed ? reinterpret_cast<int32_t*>(ws + up256(n * sizeof(int32_t))) : nullptr;
   int32_t* position =
-      tables ? reinterpret_cast<int32_t*>(ws + 2 * up256(n * sizeof(int32_t))) : nullptr;
+      listed ? reinterpret_cast<int32_t*>(ws + 2 * up256(n * sizeof(int32_t))) : nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   unsigned* err = nullptr;
@@ -330,10 +384,27 @@ int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_
     a.err = err;
     a.group = plan->chained ? kGroup : kLooseGroup;
     a.slice = plan->chained ? kSlice : kLooseSlice;
-    auto launch = [&]() {
-      const dim3 grid(static_cast<unsigned>((a.chunks * 16 + a.slice - 1) / a.slice),
-                      static_cast<unsigned>((a.n + a.group - 1) / a.group),
-                      static_cast<unsigned>(2 * a.layers));
+    auto launch = [&](bool rename) {
+      dim3 grid(static_cast<unsigned>((a.chunks * 16 + a.slice - 1) / a.slice),
+                static_cast<unsigned>((a.n + a.group - 1) / a.group),
+                static_cast<unsigned>(2 * a.layers));
+      if (rename) {
+        a.tables = static_cast<int32_t*>(block_tables->data);
+        a.rows = block_tables->shape[0];
+        a.cols = static_cast<int>(block_tables->shape[1]);
+        a.stride = block_tables->stride[0];
+        // Up to 8 entries a thread ride along (48 moves in a pool of 512 pages, 16 tables: 4.6 -> 2.9
+        // us on the device and 8.8 -> 4.7 a call against a second launch and its workspace); longer
+        // tables have a launch of their own.
+        const int64_t total = a.rows * a.cols, ride = int64_t{8 * 32} * grid.x * grid.y;
+        if (total <= ride) {
+          grid.z += 1;
+        } else if constexpr (std::is_same_v<std::decay_t<decltype(a)>, MoveArgs<kFewMoves>>) {
+          const int64_t blocks = std::min<int64_t>((total + kThreads - 1) / kThreads, 152 * 8);
+          rename_few_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a);
+          if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
+      }
       move_kernel<<<grid, 32, a.group * a.slice, st>>>(a);  // 16 or 32 KB of shared memory
       return cudaGetLastError();
     };
@@ -348,7 +419,7 @@ int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_
           a.src[i] = plan->staged[b + i];
           a.dst[i] = ~static_cast<int32_t>(b + i);
         }
-        if ((e = launch()) != cudaSuccess) return cuda_fail(e, "move_blocks staging launch");
+        if ((e = launch(false)) != cudaSuccess) return cuda_fail(e, "move_blocks staging launch");
       }
       a.position = l0 == 0 ? position : nullptr;
       for (int64_t b = 0; b < n; b += most) {
@@ -357,19 +428,20 @@ int pa_move_blocks(const pa_move_plan* plan, const pa_tensor* k_cache, const pa_
         std::copy_n(plan->src.data() + b, a.n, a.src);
         std::copy_n(plan->dst.data() + b, a.n, a.dst);
         std::copy_n(plan->id.data() + b, a.n, a.id);
-        if ((e = launch()) != cudaSuccess) return cuda_fail(e, "move_blocks launch");
+        if ((e = launch(tables && few && l0 == 0)) != cudaSuccess)
+          return cuda_fail(e, "move_blocks launch");
       }
     }
     return PA_OK;
   };
-  if (n <= kFewMoves) {
+  if (few) {
     MoveArgs<kFewMoves> a;
     if ((rc = run(a, kFewMoves))) return rc;
   } else {
     MoveArgs<kMaxMoves> a;
     if ((rc = run(a, kMaxMoves))) return rc;
   }
-  if (tables) {
+  if (listed) {
     const int64_t total = block_tables->shape[0] * block_tables->shape[1];
     const unsigned blocks = static_cast<unsigned>(
         std::min<int64_t>((total + kThreads - 1) / kThreads, 152 * 8));

@@ -93,6 +93,26 @@ def test_lists_of_several_launches(kind):
         assert torch.equal(raw(dk), moved(k, pairs)) and torch.equal(raw(dv), moved(v, pairs))
 
 
+@pytest.mark.parametrize("n, shape", [
+    (256, (3, 700)), (257, (3, 700)), (9, (300, 900)), (256, (1, 1)), (1100, (40, 50))])
+def test_tables_of_many_sizes(n, shape):
+    """Renaming beside the moves, by a launch of its own and after long lists."""
+    nb = 1500
+    rng = random.Random(n)
+    to = list(range(nb))
+    rng.shuffle(to)
+    pairs = rng.sample([(s, d) for s, d in enumerate(to) if s != d], n)
+    k, v = bits((nb, 1, 16, 64), torch.uint8, 6), bits((nb, 1, 16, 64), torch.uint8, 7)
+    dk, dv = k.cuda(), v.cuda()
+    t = torch.randint(-1, nb, shape, generator=torch.Generator().manual_seed(n), dtype=torch.int32)
+    dt = t.cuda()
+    pa.move_blocks(dk, dv, pairs, block_tables=dt)
+    assert torch.equal(raw(dk), moved(k, pairs)) and torch.equal(raw(dv), moved(v, pairs))
+    new = torch.arange(nb, dtype=torch.int32)
+    new[[s for s, _ in pairs]] = torch.tensor([d for _, d in pairs], dtype=torch.int32)
+    assert torch.equal(dt.cpu(), torch.where(t < 0, t, new[t.clamp(min=0).long()]))
+
+
 def test_layers_of_k_and_v_in_one_buffer():
     both = bits((4, 2, 30, 2, 16, 64), torch.float16, 3)
     d = both.cuda()
