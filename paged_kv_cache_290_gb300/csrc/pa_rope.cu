@@ -343,9 +343,9 @@ extern "C" int pa_rope_and_cache(const pa_tensor* q, const pa_tensor* k, const p
     if (ax < 0 || ax >= positions->shape[0])
       return fail(PA_ERR_INVALID_ARG, "axis_of_pair names an axis that positions lacks");
     // whole turns per position change nothing: keep the fraction, as an integer over 2^64
-    double turns = std::fmod(f * 0.15915494309189533577, 1.0);  // 1 / (2 pi)
-    if (turns < 0) turns += 1.0;
-    a.turn[i] = turns < 1.0 ? static_cast<uint64_t>(std::ldexp(turns, 64)) : 0;
+    double turns = f * 0.15915494309189533577;  // 1 / (2 pi)
+    turns -= std::floor(turns);
+    a.turn[i] = turns < 1.0 ? static_cast<uint64_t>(turns * 0x1p64) : 0;
     a.axis[i] = static_cast<uint8_t>(ax);
   }
   if (t == 0) return PA_OK;
