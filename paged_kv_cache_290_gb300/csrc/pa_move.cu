@@ -13,8 +13,9 @@
 //
 // Bound by HBM: each moved byte is read and written once, plus staging (about 1 in kGroup of a
 // chain's moves, read and written once more).  4096 pages of 8 layers put in order (2.1 GB, long
-// cycles) 666 us = 6.4 TB/s of moved bytes read and written, 0.96 of the measured copy rate (groups of 8 in
-// registers, a thread per 16 bytes: 729 us, an eighth of the pages staged; 16 x 2 KB 680 us).  The
+// cycles) 656 us = 6.55 TB/s of moved bytes read and written, 0.98 of the measured copy rate (with
+// launches of 1024 moves 667 us, and with those, groups of 8 in registers, a thread per 16 bytes, 729,
+// an eighth of the pages staged; 16 x 2 KB 680); 2 x 1501 holes of four E4M3 layers 62 us, 0.95.  The
 // moves travel as kernel arguments: no upload, and a captured launch keeps its own copy.
 #include <cuda_runtime.h>
 
@@ -33,9 +34,10 @@ namespace pa {
 namespace {
 
 constexpr int kGroup = 32;
-// Moves per launch, which travel as kernel arguments: 12 KB of the 32 KB there are.  A short list
+// Moves per launch, which travel as kernel arguments: 24 KB of the 32 KB there are (1501 holes 64.9 us
+// with 12 KB, 62.0 with 24).  A short list
 // takes the small size, whose arguments stay below 4 KB (a launch of the small size costs 3.0 us on the host).
-constexpr int kMaxMoves = 1024, kFewMoves = 256;
+constexpr int kMaxMoves = 2048, kFewMoves = 256;
 constexpr int kThreads = 256;  // of the renaming
 // Moves and bytes of a page per CTA: a list with chains keeps the plan's groups together; one
 // without takes smaller groups of longer slices, which start sooner (48 moves 1.3 us less, 1501
