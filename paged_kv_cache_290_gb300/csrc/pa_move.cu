@@ -34,9 +34,9 @@ namespace pa {
 namespace {
 
 constexpr int kGroup = 32;
-// Moves per launch, which travel as kernel arguments: 24 KB of the 32 KB there are (1501 holes 64.9 us
-// with 12 KB, 62.0 with 24).  A short list
-// takes the small size, whose arguments stay below 4 KB (a launch of the small size costs 3.0 us on the host).
+// Moves per launch, which travel as kernel arguments: 24 KB of the 32 KB there are (1501 holes 64.9
+// us with 12 KB, 62.0 with 24).  A short list takes the small size, whose arguments stay below 4 KB
+// (a launch of the small size costs 3.0 us on the host).
 constexpr int kMaxMoves = 2048, kFewMoves = 256;
 constexpr int kThreads = 256;  // of the renaming
 // Moves and bytes of a page per CTA: a list with chains keeps the plan's groups together; one
